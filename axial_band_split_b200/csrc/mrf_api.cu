@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "block_ops.h"
 #include "mrf_handle.h"
 
 using namespace mrf;
@@ -33,6 +34,17 @@ bool cuda_ok(mrf_handle *h, cudaError_t e, const char *what, mrf_status *st) {
   cudaGetLastError();
   return false;
 }
+
+}  // namespace
+
+void mrf::set_thread_error(const char *msg) noexcept {
+  try {
+    g_create_error = msg;
+  } catch (...) {
+  }
+}
+
+namespace {
 
 std::string validate_config(const mrf_config &c) {
   if (c.sample_rate < 8000 || c.sample_rate > 384000) return "sample_rate out of range";

@@ -7,11 +7,16 @@ there is no fallback path.
     from axial_band_split_b200 import mrf
     model = mrf.Model(cfg, weights, max_batch=1, max_frames=1100)   # weights: name -> ndarray
     masks = model.forward(stft_repr)            # torch CUDA float32 [B, F*2, T, 2]
+
+The block operators (rms_norm, rope, attention_packed) take and return torch CUDA tensors and need
+no model: they are the steps between the matrix products of a transformer block over sequences of
+different lengths packed without padding.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -28,7 +33,8 @@ EXPORTS = ["mrf_create", "mrf_forward", "mrf_forward_separate", "mrf_stft", "mrf
            "mrf_forward_host", "mrf_forward_host_async", "mrf_host_join", "mrf_sync_status", "mrf_destroy",
            "mrf_last_error", "mrf_band_tables", "mrf_set_timing", "mrf_kernel_times",
            "mrf_set_graph", "mrf_launches_per_forward", "mrf_debug_buffer", "mrf_forward_static",
-           "mrf_debug_stall_next", "mrf_chunk_plan", "mrf_separate_audio_chunked"]
+           "mrf_debug_stall_next", "mrf_chunk_plan", "mrf_separate_audio_chunked", "mrf_rms_norm",
+           "mrf_rope_table", "mrf_rope", "mrf_attention_workspace", "mrf_attention", "mrf_ops_sync_status"]
 
 
 class MrfError(RuntimeError):
@@ -52,6 +58,38 @@ class mrf_tensor(ctypes.Structure):
 
 class mrf_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int), ("ms", ctypes.c_double)]
+
+
+class mrf_rms_norm_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "out", "residual_out", "scales")] + \
+        [(n, ctypes.c_int64) for n in ("rows", "x_stride", "residual_stride", "out_stride", "residual_out_stride")] + \
+        [(n, ctypes.c_int) for n in ("dim", "dtype", "weight_dtype", "out_dtype", "group", "clamp")] + \
+        [("eps", ctypes.c_float)]
+
+
+class mrf_rope_config(ctypes.Structure):
+    _fields_ = [("part", ctypes.c_int), ("scaling", ctypes.c_int)] + \
+        [(n, ctypes.c_double) for n in ("theta", "factor", "original", "beta_fast", "beta_slow")]
+
+
+class mrf_rope_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "positions", "turns")] + \
+        [(n, ctypes.c_int64) for n in (
+            "tokens", "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride", "q_out_token_stride",
+            "q_out_head_stride", "k_out_token_stride", "k_out_head_stride")] + \
+        [(n, ctypes.c_int) for n in ("heads", "kv_heads", "width", "part", "dtype", "positions_wide", "interleaved")] + \
+        [("scale", ctypes.c_float)]
+
+
+class mrf_attention_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "q_offsets", "k_start", "k_len",
+                                               "workspace")] + \
+        [("workspace_bytes", ctypes.c_size_t)] + \
+        [(n, ctypes.c_int64) for n in (
+            "q_rows", "k_rows", "max_k", "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+            "v_token_stride", "v_head_stride", "out_token_stride", "out_head_stride")] + \
+        [(n, ctypes.c_int) for n in ("seqs", "heads", "kv_heads", "width", "v_width", "dtype", "causal")] + \
+        [("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -110,6 +148,18 @@ def lib():
         IP = ctypes.POINTER(I)
         L.mrf_chunk_plan.argtypes = [I, I, I, IP, IP, IP, IP, P, P, P, I]
         L.mrf_chunk_plan.restype = I
+        L.mrf_rms_norm.argtypes = [ctypes.POINTER(mrf_rms_norm_args), P]
+        L.mrf_rms_norm.restype = I
+        L.mrf_rope_table.argtypes = [ctypes.POINTER(mrf_rope_config), P, ctypes.POINTER(ctypes.c_float)]
+        L.mrf_rope_table.restype = I
+        L.mrf_rope.argtypes = [ctypes.POINTER(mrf_rope_args), P]
+        L.mrf_rope.restype = I
+        L.mrf_attention_workspace.argtypes = [ctypes.POINTER(mrf_attention_args), ctypes.POINTER(ctypes.c_size_t)]
+        L.mrf_attention_workspace.restype = I
+        L.mrf_attention.argtypes = [ctypes.POINTER(mrf_attention_args), P]
+        L.mrf_attention.restype = I
+        L.mrf_ops_sync_status.argtypes = [P]
+        L.mrf_ops_sync_status.restype = I
         _lib = L
     return _lib
 
@@ -170,6 +220,244 @@ def _stream_ptr(stream):
         import torch
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+# ------------------------------------------------------------------ block operators
+def _require(ok, message, status=-1):
+    if not ok:
+        raise MrfError(status, message)
+
+
+def _dtype(x, name):
+    """mrf_dtype of a CUDA tensor of one of the block operators' types; they compute no gradients."""
+    import torch
+    _require(isinstance(x, torch.Tensor) and x.is_cuda, f"{name} must be a CUDA tensor")
+    _require(not (x.requires_grad and torch.is_grad_enabled()), f"{name} requires a gradient; the library is for inference")
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(x.dtype)
+    _require(code is not None, f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    return code
+
+
+def _match(x, like, name, shape):
+    """`x` has like's type and device and the given shape, its last dimension contiguous."""
+    _require(x.is_cuda and x.device == like.device, f"{name} must be on {like.device}")
+    _require(x.dtype == like.dtype, f"{name} must be {like.dtype}, got {x.dtype}")
+    _require(tuple(x.shape) == tuple(shape), f"{name} must be {tuple(shape)}, got {tuple(x.shape)}", -2)
+    _require(x.shape[-1] <= 1 or x.stride(-1) == 1, f"{name}: the last dimension must be contiguous")
+
+
+def _index(x, like, name, count, wide=False):
+    """`x` is a contiguous int32 (or int64 where `wide`) vector of `count` values on like's device."""
+    import torch
+    _require(isinstance(x, torch.Tensor) and x.is_cuda and x.device == like.device, f"{name} must be on {like.device}")
+    _require(x.dtype == torch.int32 or (wide and x.dtype == torch.int64),
+             f"{name} must be int32{' or int64' if wide else ''}, got {x.dtype}")
+    _require(x.dim() == 1 and x.shape[0] == count and (count <= 1 or x.stride(0) == 1),
+             f"{name} must be a contiguous vector of {count} values", -2)
+
+
+def _on_device(call, x, stream):
+    """call(stream pointer) with x's device current and `stream` (a torch stream or a pointer; None: the
+    current one) as torch's current stream, so that what the call allocates belongs to it."""
+    import torch
+    if stream is None and x.device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(x.device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+        _require(stream.device == x.device, f"the stream must be on {x.device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+class RmsNorm(NamedTuple):
+    """What rms_norm returns: the normed rows; the scales of an 8-bit output, else None; h = x +
+    residual, None without a residual."""
+    out: object
+    scales: object
+    residual: object
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None, group=0, clamp=False, out=None,
+             residual_out=None, stream=None):
+    """mrf_rms_norm: h = x + residual, then h * weight / sqrt(mean h^2 + eps) over the last dimension
+    (with clamp: h * weight / max(sqrt(mean h^2), eps)).
+
+    x: CUDA float32, float16 or bfloat16 [rows, dim] (any row stride), or contiguous with more leading
+    dimensions; residual the same; weight [dim] of any of the three types.  out_dtype
+    torch.float8_e4m3fn gives 8-bit rows and float32 scales [..., ceil(dim / group)], one for each
+    `group` columns (0: the row), out * scale standing for the value.  out=x norms in place,
+    residual_out=residual updates the residual in place; without residual_out h gets a new tensor.
+    Returns RmsNorm(out, scales, residual)."""
+    import torch
+    code = _dtype(x, "x")
+    _require(x.dim() >= 1 and x.shape[-1] >= 1, "x must have a last dimension of at least 1", -2)
+    quant = out_dtype == torch.float8_e4m3fn
+    _require(quant or out_dtype is None or out_dtype == x.dtype, "out_dtype must be x's type or torch.float8_e4m3fn")
+    dim = x.shape[-1]
+    rows = x.numel() // dim
+
+    def stride(t, name):
+        _require(t.dim() == 2 or t.is_contiguous(), f"{name} with more than two dimensions must be contiguous")
+        return t.stride(0) if t.dim() == 2 else dim
+
+    _match(x, x, "x", x.shape)
+    _require(residual is not None or residual_out is None, "residual_out without residual")
+    wcode = 0
+    if weight is not None:
+        wcode = _dtype(weight, "weight")
+        _require(weight.device == x.device and tuple(weight.shape) == (dim,) and (dim == 1 or weight.stride(0) == 1),
+                 f"weight must be a contiguous [{dim}] on {x.device}", -2)
+    if residual is not None:
+        _dtype(residual, "residual")
+        _match(residual, x, "residual", x.shape)
+
+    def call(st):
+        o = torch.empty(x.shape, dtype=torch.float8_e4m3fn if quant else x.dtype, device=x.device) if out is None else out
+        if out is not None:
+            _require(o.dtype == (torch.float8_e4m3fn if quant else x.dtype), f"out has the wrong type, {o.dtype}")
+            _match(o, o, "out", x.shape)
+            _require(o.device == x.device, f"out must be on {x.device}")
+        scales = torch.empty(x.shape[:-1] + (-(-dim // group) if group > 0 else 1,), dtype=torch.float32,
+                             device=x.device) if quant else None
+        h = residual_out
+        if residual is not None:
+            if h is None:
+                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            _match(h, x, "residual_out", x.shape)
+        a = mrf_rms_norm_args(
+            x.data_ptr(), residual.data_ptr() if residual is not None else None,
+            weight.data_ptr() if weight is not None else None, o.data_ptr(), h.data_ptr() if h is not None else None,
+            scales.data_ptr() if quant else None, rows, stride(x, "x"),
+            stride(residual, "residual") if residual is not None else 0, stride(o, "out"),
+            stride(h, "residual_out") if h is not None else 0, dim, code, wcode, 3 if quant else code, group,
+            int(clamp), eps)
+        _check(lib().mrf_rms_norm(ctypes.byref(a), st))
+        return RmsNorm(o, scales, h)
+
+    return _on_device(call, x, stream)
+
+
+class RopeTable(NamedTuple):
+    """Rotary frequencies of `part` dimensions on one device: turns (int64 [part / 2], binary fractions
+    of a turn a position) and the factor on cos and sin."""
+    turns: object
+    scale: float
+    part: int
+
+
+def rope_table(part, theta=10000.0, scaling="none", factor=1.0, original=0, beta_fast=0.0, beta_slow=0.0, device="cuda"):
+    """mrf_rope_table: the frequencies theta^(-2i / part), scaled for contexts longer than the training's
+    by "linear" (positions / factor), "ntk" (a larger theta) or "yarn" (by parts; `original` is the
+    training's context length).  Made once and kept; rope takes it."""
+    import torch
+    kinds = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+    _require(scaling in kinds, f"scaling must be one of {sorted(kinds)}, got {scaling!r}")
+    c = mrf_rope_config(part, kinds[scaling], theta, factor, original, beta_fast, beta_slow)
+    turns = np.zeros(max(1, min(part, 1024) // 2), np.uint64)
+    scale = ctypes.c_float(0)
+    _check(lib().mrf_rope_table(ctypes.byref(c), turns.ctypes.data_as(ctypes.c_void_p), ctypes.byref(scale)))
+    return RopeTable(torch.from_numpy(turns.view(np.int64)).to(device), scale.value, part)
+
+
+def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, stream=None):
+    """mrf_rope: the first table.part dimensions of every head of q [tokens, heads, width] and of k
+    [tokens, kv_heads, width] (or None) turned by each token's position (int32 or int64 [tokens]), in pairs
+    (2i, 2i + 1), or (i, i + part / 2) with interleaved=False.  Heads and tokens may have any strides
+    (column ranges of a projection's rows); q_out=q and k_out=k turn in place.  Returns (q_out, k_out)."""
+    import torch
+    code = _dtype(q, "q")
+    _require(q.dim() == 3, f"q must be [tokens, heads, width], got {tuple(q.shape)}", -2)
+    _match(q, q, "q", q.shape)
+    tokens, heads, width = q.shape
+    kv_heads = 0
+    if k is not None:
+        _dtype(k, "k")
+        _require(k.dim() == 3, f"k must be [tokens, kv_heads, width], got {tuple(k.shape)}", -2)
+        kv_heads = k.shape[1]
+        _match(k, q, "k", (tokens, kv_heads, width))
+    _require(k is not None or k_out is None, "k_out without k")
+    _index(positions, q, "positions", tokens, wide=True)
+    _require(isinstance(table, RopeTable), "table must come from rope_table")
+    _require(table.turns.device == q.device, f"the table must be on {q.device}")
+
+    def call(st):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _match(qo, q, "q_out", q.shape)
+        ko = k_out
+        if k is not None:
+            if ko is None:
+                ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            _match(ko, k, "k_out", k.shape)
+        a = mrf_rope_args(
+            q.data_ptr(), k.data_ptr() if kv_heads else None, qo.data_ptr(), ko.data_ptr() if kv_heads else None,
+            positions.data_ptr(), table.turns.data_ptr(), tokens, q.stride(0), q.stride(1),
+            k.stride(0) if kv_heads else 0, k.stride(1) if kv_heads else 0, qo.stride(0), qo.stride(1),
+            ko.stride(0) if kv_heads else 0, ko.stride(1) if kv_heads else 0, heads, kv_heads, width, table.part, code,
+            int(positions.dtype == torch.int64), int(interleaved), table.scale)
+        _check(lib().mrf_rope(ctypes.byref(a), st))
+        return qo, ko
+
+    return _on_device(call, q, stream)
+
+
+def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, causal=True, scale=None, out=None,
+                     return_lse=False, stream=None):
+    """mrf_attention: softmax attention with grouped heads over sequences packed one after another.
+
+    q [q_rows, heads, width], k [k_rows, kv_heads, width], v [k_rows, kv_heads, v_width]: CUDA float16,
+    bfloat16 or float32 with any token and head strides.  Sequence b owns the query rows q_offsets[b] ..
+    q_offsets[b + 1] (int32 [seqs + 1]) and the key rows k_start[b] .. k_start[b] + k_len[b] (int32 [seqs];
+    without them its query rows).  causal: the last query sees all keys of its sequence.  max_k: an upper
+    bound of the key counts known on the host (0: k's rows), which only decides how the work is split.
+    Rows of no sequence keep what `out` held (a new `out` is uninitialised there).  Returns out
+    [q_rows, heads, v_width], or (out, lse float32 [q_rows, heads]) with return_lse."""
+    import torch
+    code = _dtype(q, "q")
+    _require(q.dim() == 3, f"q must be [q_rows, heads, width], got {tuple(q.shape)}", -2)
+    _dtype(k, "k")
+    _dtype(v, "v")
+    _require(k.dim() == 3 and v.dim() == 3, "k and v must be [k_rows, kv_heads, width]", -2)
+    q_rows, heads, width = q.shape
+    k_rows, kv_heads, v_width = v.shape
+    _match(q, q, "q", q.shape)
+    _match(k, q, "k", (k_rows, kv_heads, width))
+    _match(v, q, "v", v.shape)
+    _require(isinstance(q_offsets, torch.Tensor) and q_offsets.dim() == 1 and q_offsets.shape[0] >= 1,
+             "q_offsets must be [seqs + 1]", -2)
+    seqs = q_offsets.shape[0] - 1
+    _index(q_offsets, q, "q_offsets", seqs + 1)
+    _require((k_start is None) == (k_len is None), "k_start and k_len go together")
+    if k_len is not None:
+        _index(k_start, q, "k_start", seqs)
+        _index(k_len, q, "k_len", seqs)
+
+    def call(st):
+        o = torch.empty((q_rows, heads, v_width), dtype=q.dtype, device=q.device) if out is None else out
+        _match(o, q, "out", (q_rows, heads, v_width))
+        lse = torch.empty((q_rows, heads), dtype=torch.float32, device=q.device) if return_lse else None
+        a = mrf_attention_args(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr() if return_lse else None,
+            q_offsets.data_ptr(), k_start.data_ptr() if k_len is not None else None,
+            k_len.data_ptr() if k_len is not None else None, None, 0, q_rows, k_rows, max_k, q.stride(0), q.stride(1),
+            k.stride(0), k.stride(1), v.stride(0), v.stride(1), o.stride(0), o.stride(1), seqs, heads, kv_heads, width,
+            v_width, code, int(causal), width ** -0.5 if scale is None else scale)
+        need = ctypes.c_size_t(0)
+        _check(lib().mrf_attention_workspace(ctypes.byref(a), ctypes.byref(need)))
+        if need.value:
+            space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+            a.workspace, a.workspace_bytes = space.data_ptr(), need.value
+        _check(lib().mrf_attention(ctypes.byref(a), st))
+        return (o, lse) if return_lse else o
+
+    return _on_device(call, q, stream)
+
+
+def ops_sync_status(stream=None):
+    """mrf_ops_sync_status: wait for `stream` and raise if a block operator's kernel gave up a wait."""
+    _check(lib().mrf_ops_sync_status(_stream_ptr(stream)))
 
 
 class Model:

@@ -50,7 +50,8 @@ typedef enum {
   MRF_FP32_DEBUG = 2      /* fp32 CUDA-core schedule, unfused, for debugging and tight parity */
 } mrf_compute;
 
-typedef enum { MRF_DTYPE_F32 = 0, MRF_DTYPE_F16 = 1 } mrf_dtype;
+/* Weights (mrf_tensor) are F32 or F16; the block operators below take the others too. */
+typedef enum { MRF_DTYPE_F32 = 0, MRF_DTYPE_F16 = 1, MRF_DTYPE_BF16 = 2, MRF_DTYPE_E4M3 = 3 } mrf_dtype;
 
 /* Model configuration: the fields of the checkpoint's config.json.  All sizes explicit. */
 typedef struct {
@@ -333,6 +334,152 @@ mrf_status mrf_debug_buffer(mrf_handle *h, const char *name, void *host_dst, siz
 
 /* Number of kernels one mrf_forward launches for (B, T). */
 int mrf_launches_per_forward(const mrf_handle *h, int B, int T);
+
+/*
+ * Block operators: the steps between the matrix products of a transformer block, for a caller
+ * that runs its own projections (a causal or streaming variant of the model, clips of different
+ * lengths packed into one batch without padding, new frames over a cache).  They use no handle.
+ * Every pointer below is a device pointer on the current device unless it says host; the work is
+ * queued on `stream`, nothing is allocated, nothing waits, and every call may be captured into a
+ * CUDA graph (pointers and sizes are then those of the capture; offsets, lengths and positions
+ * are read from device memory when the work runs).  Strides count elements; the innermost
+ * dimension is contiguous.  Arguments are checked before anything is launched; the text of a
+ * failure is in mrf_last_error(NULL) of the calling thread.  Calls from several threads and on
+ * several streams do not disturb one another as long as their outputs and workspaces are their
+ * own.  They compute outputs only, no gradients: the library is for inference.
+ */
+
+/*
+ * mrf_rms_norm - h = x + residual (x alone when residual is NULL), then
+ *   out[r, j] = h[r, j] * weight[j] * s_r,   s_r = 1 / sqrt(mean_j h^2 + eps), or with clamp
+ *   s_r = 1 / max(sqrt(mean_j h^2), eps) (the model's own norm sqrt(dim) x / max(|x|, 1e-12) is
+ *   clamp with eps = 1e-12 / sqrt(dim)).
+ * h is formed, squared and summed in fp32 and rounded once where it is stored as residual_out.
+ * With out_dtype MRF_DTYPE_E4M3 the output is 8-bit: scales[r, g] = max |y| / 448 over each group
+ * of `group` columns (0: the whole row; the last group may be short) of y = the formula above,
+ * and out = y / scales[r, g] rounded to the nearest e4m3 (ties to even); a group of zeros has
+ * scale 0 and codes 0, a row with a NaN or an infinity NaN scales and codes.
+ * out may be x, and residual_out may be residual (same pointer, stride and type); any other overlap is undefined.
+ * Rows whose sum of squares passes the fp32 range are not supported (x beyond about 1e18).
+ */
+typedef struct {
+  const void *x;         /* dtype [rows, dim] */
+  const void *residual;  /* dtype [rows, dim], or NULL */
+  const void *weight;    /* weight_dtype [dim], or NULL (ones) */
+  void *out;             /* out_dtype [rows, dim] */
+  void *residual_out;    /* dtype [rows, dim]: h; NULL: not stored.  Needs residual */
+  float *scales;         /* [rows, ceil(dim / group)] contiguous; NULL unless out_dtype is E4M3 */
+  int64_t rows;          /* 0: nothing is launched */
+  int64_t x_stride, residual_stride, out_stride, residual_out_stride; /* elements between rows */
+  int dim;               /* 1 .. 16384 */
+  int dtype;             /* F32, F16 or BF16 */
+  int weight_dtype;      /* F32, F16 or BF16 */
+  int out_dtype;         /* dtype, or E4M3 */
+  int group;             /* E4M3: 0, 32, 64 or 128 columns a scale */
+  int clamp;
+  float eps;             /* > 0 */
+} mrf_rms_norm_args;
+mrf_status mrf_rms_norm(const mrf_rms_norm_args *a, void *stream);
+
+/*
+ * mrf_rope_table - host only: the frequency table of rotary positions over `part` dimensions.
+ * Frequency i of part / 2 is f_i = theta^(-2i / part) radians a position, changed by `scaling`:
+ *   MRF_ROPE_LINEAR  f_i / factor;
+ *   MRF_ROPE_NTK     theta * factor^(part / (part - 2)) in place of theta (part > 2);
+ *   MRF_ROPE_YARN    by parts: with d(t) = part * ln(original / (2 pi t)) / (2 ln theta), the
+ *                    dimension that turns t times in `original` positions, lo = max(floor
+ *                    d(beta_fast), 0), hi = min(ceil d(beta_slow), part - 1) and r_i = (i - lo) /
+ *                    max(hi - lo, 0.001) held to [0, 1]: f_i (1 - r_i) + f_i / factor * r_i, and
+ *                    cos and sin times 0.1 ln(factor) + 1 (factor > 1).
+ * turns[i] (part / 2 values, host) receives f_i / (2 pi) as a 64-bit binary fraction of a turn:
+ * position * turns[i] modulo 2^64 is the angle's fraction of a turn with no error that grows into
+ * the result at any position below 2^40.  *scale receives the factor on cos and sin.
+ */
+typedef enum { MRF_ROPE_NONE = 0, MRF_ROPE_LINEAR = 1, MRF_ROPE_NTK = 2, MRF_ROPE_YARN = 3 } mrf_rope_scaling;
+typedef struct {
+  int part;                    /* even, 2 .. 1024 */
+  int scaling;                 /* mrf_rope_scaling */
+  double theta;                /* > 1 */
+  double factor;               /* >= 1; LINEAR, NTK and YARN */
+  double original;             /* YARN: the context length of training, >= 1 */
+  double beta_fast, beta_slow; /* YARN: turns; 0, 0: 32 and 1 */
+} mrf_rope_config;
+mrf_status mrf_rope_table(const mrf_rope_config *c, uint64_t *turns, float *scale);
+
+/*
+ * mrf_rope - rotates the first `part` of the `width` dimensions of every head of q, and of k when
+ * it is given, by the token's position: pairs (2i, 2i + 1) with interleaved (the model's layout),
+ * else (i, i + part / 2), (a, b) -> scale * (a cos - b sin, b cos + a sin); the other dimensions are
+ * copied.  Rotations are computed in fp32 and rounded once.  q_out may be q and k_out may be k
+ * (same pointer, strides); any other overlap is undefined.  Negative positions turn backwards
+ * (the inverse rotation).
+ */
+typedef struct {
+  const void *q, *k;         /* dtype [tokens, heads, width], [tokens, kv_heads, width]; k NULL: none */
+  void *q_out, *k_out;
+  const void *positions;     /* [tokens], int32 or int64 */
+  const uint64_t *turns;     /* device copy of mrf_rope_table's, part / 2 values */
+  int64_t tokens;            /* 0: nothing is launched */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+  int heads, kv_heads;       /* kv_heads 0 when k is NULL */
+  int width, part;           /* part even, 2 .. width; width up to 1024 */
+  int dtype;                 /* F32, F16 or BF16 */
+  int positions_wide;        /* 1: int64 positions, 0: int32 */
+  int interleaved;
+  float scale;
+} mrf_rope_args;
+mrf_status mrf_rope(const mrf_rope_args *a, void *stream);
+
+/*
+ * mrf_attention - softmax(scale q k^T) v over packed sequences with grouped heads: query head h
+ * reads key head h / (heads / kv_heads).  Sequence b has the query rows q_offsets[b] ..
+ * q_offsets[b + 1] and the key rows k_start[b] .. k_start[b] + k_len[b] (k_start and k_len NULL:
+ * its query rows, a whole prompt).  causal: the last query sees every key and query i of n_q sees
+ * the keys up to i + n_k - n_q, so the same call serves a prompt, a prompt's next piece over a
+ * cache, and one new token.  A query that sees no key gets out 0 and lse -inf.  lse (NULL: not
+ * stored) is ln sum exp(scale q k) in natural units.  Scores, softmax statistics and sums are
+ * fp32; the probabilities are rounded to the tensors' type for the second product (in fp32 for
+ * F32), the output once.  Key rows outside a sequence are never used, whatever they hold; inside it
+ * keys masked by causality may be anything, but their values must be finite.  Rows
+ * of out and lse that belong to no sequence are left as they were.  Offsets are read on the
+ * device and held to the tensors' rows, so wrong ones give wrong rows but no access outside.
+ *
+ * F16 and BF16 with widths up to 128 run on the tensor cores when q, k, v and out are 16-byte
+ * aligned with widths and strides that are multiples of 8 elements; anything else (F32, odd widths,
+ * up to 256) runs on the CUDA cores.
+ *
+ * workspace: device memory of at least the bytes mrf_attention_workspace gives for the same
+ * arguments (which may be 0), 16-byte aligned, the call's own until the work has run.  max_k, an upper bound
+ * of the sequences' key counts, decides only how the work is split, never the result's rows.
+ */
+typedef struct {
+  const void *q, *k, *v;         /* dtype [q_rows, heads, width], [k_rows, kv_heads, width], [k_rows, kv_heads, v_width] */
+  void *out;                     /* dtype [q_rows, heads, v_width]; must not overlap the inputs */
+  float *lse;                    /* [q_rows, heads] contiguous, or NULL */
+  const int32_t *q_offsets;      /* [seqs + 1], ascending */
+  const int32_t *k_start, *k_len; /* [seqs] each, or both NULL */
+  void *workspace;
+  size_t workspace_bytes;
+  int64_t q_rows, k_rows;        /* each below 2^31; q_rows 0: nothing is launched */
+  int64_t max_k;                 /* 0: k_rows */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+  int seqs, heads, kv_heads;     /* heads a multiple of kv_heads; seqs 0: nothing is launched */
+  int width, v_width;            /* 1 .. 256 */
+  int dtype;                     /* F32, F16 or BF16 */
+  int causal;
+  float scale;                   /* > 0; usually width^-1/2 */
+} mrf_attention_args;
+mrf_status mrf_attention_workspace(const mrf_attention_args *a, size_t *bytes);
+mrf_status mrf_attention(const mrf_attention_args *a, void *stream);
+
+/*
+ * mrf_ops_sync_status - wait for `stream`, then report the block operators' status on the current
+ * device as mrf_sync_status does for a handle: MRF_OK, MRF_ETIMEOUT if a kernel's bounded wait
+ * expired since the last call (the word is cleared), or MRF_ECUDA.
+ */
+mrf_status mrf_ops_sync_status(void *stream);
 
 #ifdef __cplusplus
 }
