@@ -43,5 +43,12 @@ cudaError_t launch_rms_norm(const mrf_rms_norm_args &a, cudaStream_t st);
 cudaError_t launch_rope(const mrf_rope_args &a, cudaStream_t st);
 // CUDA-core attention (k_attn_rows.cu): any type, width and stride.
 cudaError_t launch_attention_rows(const mrf_attention_args &a, cudaStream_t st);
+// Tensor-core attention (k_attn_packed_tc.cu): whether it takes these arguments, the workspace it
+// needs for them, and its launches (false: a tensor map was refused and nothing was queued).
+bool attention_tc_takes(const mrf_attention_args &a);
+size_t attention_tc_workspace(const mrf_attention_args &a);
+bool launch_attention_packed_tc(const mrf_attention_args &a, cudaStream_t st, cudaError_t *err);
+// Its status word (0, or 1 and the site of a wait that expired) after the work queued on st; cleared.
+cudaError_t attention_tc_status(unsigned *word, cudaStream_t st);
 
 }  // namespace mrf

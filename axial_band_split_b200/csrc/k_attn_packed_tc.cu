@@ -1,0 +1,834 @@
+// Packed attention with grouped heads on tcgen05 tensor cores (mrf_attention): o = softmax(scale q
+// k^T) v per sequence and head, widths up to 128, fp16 or bf16, causal or not, over the query's own
+// rows or a cache.  One pass over the keys with a running maximum and sum; the scores never leave
+// the SM.
+//
+// Tiles.  The G = heads / kv_heads query heads that share a key head are rows of one matrix: a tile
+// is TQ = 128 / G tokens x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
+// box per 64 dimensions), so each key block is read once for all of them and a single new token
+// already fills G rows.  Key blocks are 128 rows.
+//
+// Work items.  A CTA runs two units (a tile with a range of keys) t = 0, 1 side by side:
+//   pair   - two neighbouring tiles of one sequence and key head: they share every key block;
+//   heads  - a sequence's odd tile (its first, which sees the fewest keys) for two key heads, each
+//            unit with its own keys: short prompts and single tokens have nothing but these;
+//   splits - with few tiles and long keys, two key ranges of one tile: every range leaves its own
+//            output and log-sum in the workspace, and combine_kernel joins them.
+// Items are numbered sequence by sequence, a causal sequence's last tiles (the most keys) first, and
+// taken round robin by persistent CTAs.  Lengths live in device memory, so warp 11 finds each item's
+// sequence by a running prefix sum over the sequences' item counts and hands it to the others
+// through a ring in shared memory.
+//
+// Warps 0-3 and 4-7: softmax of unit 0 and 1, one score row per thread; warp 8: bulk tensor loads;
+// warps 9, 10: matrix instructions of unit 0, 1; warp 11: items.  Tensor memory (512 columns): with
+// v up to 64 wide S_t at 128 t, O_t at 256 + 64 t, P_t at 384 + 64 t; with wider v S_t at 128 t and
+// O_t at 256 + 128 t, and P_t (16-bit, half as wide) overwrites S_t once the softmax has read it.
+//
+// Key rows past a sequence's end belong to others or were never written: their scores are replaced
+// by -inf whatever they are, and their rows of v, whose product with a zero probability could still
+// be NaN, are zeroed in shared memory before the second product.
+#include <algorithm>
+#include <cmath>
+
+#include "block_ops.h"
+#include "gemm_tc.cuh"
+#include "tc_ptx.cuh"
+
+namespace mrf {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128, kAtom = 16384;  // one atom: 128 rows x 64 16-bit values
+constexpr int kThreads = 384;
+// register split, as in the model's attention: 2 * 128 * 208 + 128 * 72 <= 384 * 168
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
+constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
+constexpr int kItems = 4;            // ring of work items
+
+// One unit of an item.  Token i of the tile sees the first min(klen, lim0 + i) keys of its range.
+struct Unit {
+  int q_row, ntok;   // the tile's first query row, its tokens (0: no unit)
+  int kvh;
+  int k_row, klen;   // the range's first key row, its keys
+  int lim0;
+  int nblk;          // key blocks that any of its tokens sees
+  int split;
+};
+struct Item {
+  Unit u[2];
+  int shared;  // both units read the same key blocks
+  int last;    // no more items
+};
+
+template <int QA, int VA>
+struct Cfg {
+  static constexpr bool overlay = VA == 2;           // P over S in tensor memory
+  static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
+  static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
+  static constexpr int slots = 10 * kAtom / slot;    // ring of K or V blocks
+  static constexpr int q = 0;
+  static constexpr int kv = 4 * kAtom;
+  static constexpr int bar = kv + slots * slot;
+  static constexpr int item = bar + 512;
+  static constexpr int total = item + kItems * (int)sizeof(Item) + 16;
+};
+static_assert(Cfg<1, 1>::total + 1024 <= 232448 && Cfg<2, 2>::total + 1024 <= 232448 && Cfg<2, 1>::total + 1024 <= 232448 &&
+                  Cfg<1, 2>::total + 1024 <= 232448,
+              "shared memory over the 227 KB limit");
+
+struct Args {
+  void *out;
+  float *lse;         // or null
+  float *part;        // splits: [split][row * heads + head][v_width], then their log2 sums
+  float *part_lse;
+  const int32_t *q_offsets, *k_start, *k_len;
+  long long out_token_stride, out_head_stride;
+  int q_rows, k_rows, seqs, heads, kv_heads, G, TQ, width, v_width, causal, splits;
+  float scale, scale_log2;
+};
+
+__device__ unsigned g_status[2];  // a bounded wait that expired: 1, site
+
+// ------------------------------------------------------------------ small device helpers
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <bool kBF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kBF) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+  } else {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+  }
+}
+
+// 32 fp32 columns of this thread's lane, not waited for; tmem_landed orders every use after the wait.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_landed(uint32_t *r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (+)= A * B with A (16-bit pairs) in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc ? 1u : 0u));
+}
+
+// V as the MN-major B operand: 64-wide atoms of 16 KB side by side (the leading offset), 8 keys each
+// 1024 bytes (the stride offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kAtom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Wait, within the limit, for a phase whose copies are in flight, whatever the abort flag says.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+  const unsigned long long t0 = tc::globaltimer();
+  while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {
+  }
+}
+
+// ------------------------------------------------------------------ sequences and items
+struct Seq {
+  int q0, nq, k0, nk;
+};
+// Sequence b's rows, held to the tensors' whatever the offsets say.
+__device__ __forceinline__ Seq load_seq(const Args &a, int b) {
+  Seq s;
+  s.q0 = min(max(a.q_offsets[b], 0), a.q_rows);
+  s.nq = min(max(a.q_offsets[b + 1], s.q0), a.q_rows) - s.q0;
+  if (a.k_len) {
+    s.k0 = min(max(a.k_start[b], 0), a.k_rows);
+    s.nk = min(max(a.k_len[b], 0), a.k_rows - s.k0);
+  } else {
+    s.k0 = s.q0;
+    s.nk = s.nq;
+  }
+  return s;
+}
+__device__ __forceinline__ int seq_items(const Args &a, int nq) {
+  const int nt = (nq + a.TQ - 1) / a.TQ;
+  if (a.splits > 1) return nt * a.kv_heads * (a.splits / 2);
+  return a.kv_heads * (nt / 2) + (nt & 1) * ((a.kv_heads + 1) / 2);
+}
+__device__ __forceinline__ Unit make_unit(const Args &a, const Seq &s, int tile, int kvh, int split) {
+  Unit u;
+  const int t0 = tile * a.TQ;
+  // a split's keys: whole blocks, the last one what is left
+  const int chunk = a.splits > 1 ? ((s.nk + a.splits - 1) / a.splits + kKeys - 1) / kKeys * kKeys : s.nk;
+  const int r0 = (int)min((long long)split * chunk, (long long)s.nk);
+  u.q_row = s.q0 + t0;
+  u.ntok = min(a.TQ, s.nq - t0);
+  u.kvh = kvh;
+  u.k_row = s.k0 + r0;
+  u.klen = min(s.nk - r0, chunk);
+  u.lim0 = a.causal ? (t0 - s.nq) + 1 + (s.nk - r0) : u.klen;
+  u.nblk = (max(0, min(u.klen, u.lim0 + u.ntok - 1)) + kKeys - 1) / kKeys;
+  u.split = split;
+  return u;
+}
+__device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
+  Item it;
+  const int nt = (s.nq + a.TQ - 1) / a.TQ;
+  it.last = 0;
+  it.shared = 0;
+  if (a.splits > 1) {
+    const int js = a.splits / 2, j = r % js, th = r / js;
+    const int tile = nt - 1 - th / a.kv_heads, kvh = th % a.kv_heads;
+    it.u[0] = make_unit(a, s, tile, kvh, 2 * j);
+    it.u[1] = make_unit(a, s, tile, kvh, 2 * j + 1);
+  } else if (r < a.kv_heads * (nt / 2)) {
+    const int tile = (nt & 1) + 2 * (nt / 2 - 1 - r / a.kv_heads), kvh = r % a.kv_heads;
+    it.shared = 1;
+    it.u[0] = make_unit(a, s, tile, kvh, 0);
+    it.u[1] = make_unit(a, s, tile + 1, kvh, 0);
+  } else {
+    const int kvh = 2 * (r - a.kv_heads * (nt / 2));
+    it.u[0] = make_unit(a, s, 0, kvh, 0);
+    it.u[1] = it.u[0];
+    it.u[1].kvh = kvh + 1;
+    if (kvh + 1 >= a.kv_heads) it.u[1].ntok = it.u[1].nblk = 0;
+  }
+  return it;
+}
+
+// Order of an item's ring slots.  Each unit's key stream is K0 K1 V0 K2 V1 ... V(n-1): element i of it.
+__device__ __forceinline__ int k_elem(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_elem(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+// Separate keys: the two streams take turns while both last.
+__device__ __forceinline__ int slot_of(const Item &it, int t, int e) {
+  if (it.shared) return e;
+  return t == 0 ? e + min(e, 2 * it.u[1].nblk) : e + min(e + 1, 2 * it.u[0].nblk);
+}
+__device__ __forceinline__ int item_slots(const Item &it) {
+  return it.shared ? 2 * max(it.u[0].nblk, it.u[1].nblk) : 2 * (it.u[0].nblk + it.u[1].nblk);
+}
+
+// ------------------------------------------------------------------ softmax of one key block
+__device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
+  float ma = s[0], mb = s[32], mc = s[64], md = s[96];
+#pragma unroll
+  for (int i = 1; i < 32; i += 2) {
+    const int i2 = i + 1 < 32 ? i + 1 : i;
+    ma = max3(ma, s[i], s[i2]);
+    mb = max3(mb, s[32 + i], s[32 + i2]);
+    mc = max3(mc, s[64 + i], s[64 + i2]);
+    md = max3(md, s[96 + i], s[96 + i2]);
+  }
+  return fmaxf(fmaxf(ma, mb), fmaxf(mc, md));
+}
+
+// ------------------------------------------------------------------ the kernel
+template <bool kBF, int QA, int VA>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_packed_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const Args a) {
+  using C = Cfg<QA, VA>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bar);
+  uint64_t *q_full = bars, *q_empty = bars + 2;          // [qbufs]
+  uint64_t *s_full = bars + 4, *s_free = bars + 6;       // [2]: scores written / read
+  uint64_t *p_full = bars + 8, *pv_done = bars + 10;     // [2]
+  uint64_t *o_free = bars + 12;                          // [2]
+  uint64_t *item_full = bars + 14, *item_empty = bars + 18;  // [kItems]
+  uint64_t *done = bars + 22;
+  uint64_t *kv_full = bars + 23, *kv_empty = kv_full + C::slots;
+  static_assert(23 + 2 * C::slots <= 62, "barrier area");
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 62);
+  volatile int *abort = reinterpret_cast<int *>(bars + 63);
+  Item *items = reinterpret_cast<Item *>(smem + C::item);
+  unsigned *status = g_status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int b = 0; b < C::qbufs; ++b) { tc::mbar_init(q_full + b, 1); tc::mbar_init(q_empty + b, 2); }
+    for (int s = 0; s < C::slots; ++s) { tc::mbar_init(kv_full + s, 1); tc::mbar_init(kv_empty + s, 2); }
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(s_full + t, 1);
+      tc::mbar_init(s_free + t, 4);
+      tc::mbar_init(p_full + t, 4);
+      tc::mbar_init(pv_done + t, 1);
+      tc::mbar_init(o_free + t, 4);
+    }
+    for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 11); }
+    tc::mbar_init(done, 2);
+    tc::fence_barrier_init();
+  }
+  if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  constexpr uint32_t kOCol = 256, kOStep = 64 * VA;
+
+  // the n-th item, copied from the ring; false when there is none left or a wait expired
+  auto next_item = [&](int n, Item &it) {
+    if (!tc::mbar_wait(item_full + n % kItems, (n / kItems) & 1, status, 50, abort)) return false;
+    it = items[n % kItems];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(item_empty + n % kItems);
+    return !it.last;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIo));
+    if (warp == 11) {
+      // ---------------- items: a running prefix sum over 32 sequences at a time
+      int base = 0;
+      long long before = 0, total = 0, incl = 0;  // 64 bits: wrong offsets may count rows many times
+      Seq s = {};
+      auto load = [&]() {
+        long long cnt = 0;
+        if (base + lane < a.seqs) {
+          s = load_seq(a, base + lane);
+          cnt = seq_items(a, s.nq);
+        }
+        incl = cnt;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+      };
+      load();
+      int n = 0;
+      for (long long it = blockIdx.x;; it += gridDim.x, ++n) {
+        while (base < a.seqs && it >= before + total) {
+          base += 32;
+          before += total;
+          load();
+        }
+        const bool last = base >= a.seqs;
+        Item item;
+        if (!last) {
+          const long long r = it - before;
+          const int src = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
+          Seq q;
+          q.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+          q.nq = __shfl_sync(0xffffffffu, s.nq, src);
+          q.k0 = __shfl_sync(0xffffffffu, s.k0, src);
+          q.nk = __shfl_sync(0xffffffffu, s.nk, src);
+          item = make_item(a, q, (int)(r - (__shfl_sync(0xffffffffu, incl, src) - seq_items(a, q.nq))));
+        }
+        item.last = last;
+        if (!tc::mbar_wait(item_empty + n % kItems, ((n / kItems) & 1) ^ 1, status, 51, abort)) break;
+        if (lane == 0) {
+          items[n % kItems] = item;
+          tc::mbar_arrive(item_full + n % kItems);
+        }
+        __syncwarp();
+        if (last) break;
+      }
+    } else if (warp == 8) {
+      // ---------------- bulk tensor loads
+      Item it;
+      int g = 0, qn = 0;  // ring slots filled, q buffers filled
+      const uint32_t q_bytes = (uint32_t)(a.TQ * a.G) * 128 * QA;
+      bool ok = true;
+      for (int n = 0; ok && next_item(n, it); ++n) {
+        const int n0 = it.u[0].nblk, n1 = it.u[1].nblk;
+        if (lane == 0 && n0 + n1 > 0) {
+          const int qb = qn % C::qbufs;
+          if (!tc::mbar_wait(q_empty + qb, ((qn / C::qbufs) & 1) ^ 1, status, 52, abort)) ok = false;
+          if (ok) {
+            tc::mbar_arrive_expect_tx(q_full + qb, q_bytes * ((n0 > 0) + (n1 > 0)));
+            for (int t = 0; t < 2; ++t)
+              if (it.u[t].nblk > 0)
+#pragma unroll
+                for (int c = 0; c < QA; ++c)
+                  tc::tma_load_4d(smem + C::q + ((qb * 2 + t) * QA + c) * kAtom, &tq, q_full + qb, 64 * c, 0, it.u[t].kvh,
+                                  it.u[t].q_row);
+          }
+          // element e of unit t's stream into the next slot
+          auto fill = [&](int t, int e, int nb) {
+            const int s = g % C::slots;
+            if (!tc::mbar_wait(kv_empty + s, ((g / C::slots) & 1) ^ 1, status, 53, abort)) return false;
+            const bool is_k = e == 0 || ((e & 1) && e != 2 * nb - 1);
+            const int j = is_k ? (e + 1) / 2 : e == 2 * nb - 1 ? nb - 1 : e / 2 - 1;
+            tc::mbar_arrive_expect_tx(kv_full + s, (is_k ? QA : VA) * kAtom);
+            for (int c = 0; c < (is_k ? QA : VA); ++c)
+              tc::tma_load_3d(smem + C::kv + s * C::slot + c * kAtom, is_k ? &tk : &tv, kv_full + s, 64 * c, it.u[t].kvh,
+                              it.u[t].k_row + j * kKeys);
+            ++g;
+            return true;
+          };
+          if (it.shared) {
+            const int nb = max(n0, n1);
+            for (int e = 0; ok && e < 2 * nb; ++e) ok = fill(0, e, nb);
+          } else {
+            for (int e = 0; ok && e < 2 * max(n0, n1); ++e) {
+              if (e < 2 * n0) ok = fill(0, e, n0);
+              if (ok && e < 2 * n1) ok = fill(1, e, n1);
+            }
+          }
+          ++qn;
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      }
+      if (*abort && lane == 0) {  // gave up: the copies in flight land before the memory is given back
+        for (int b = 0; b < C::qbufs && b < qn; ++b) drain(q_full + b, ((qn - 1 - b) / C::qbufs) & 1);
+        for (int i = 0; i < C::slots && i < g; ++i) drain(kv_full + (g - 1 - i) % C::slots, ((g - 1 - i) / C::slots) & 1);
+      }
+    } else {
+      // ---------------- matrix instructions of unit t
+      const int t = warp - 9;
+      Item it;
+      const uint32_t id_s = tc::idesc_f16(kRows, kKeys, false, kBF);
+      const uint32_t id_pv = tc::idesc_f16(kRows, (a.v_width + 15) / 16 * 16, true, kBF);
+      const int qk_steps = (a.width + 15) / 16;
+      const uint32_t tS = tmem + 128 * t, tO = tmem + kOCol + kOStep * t;
+      const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
+      int g0 = 0, qn = 0, blk = 0, units = 0;  // ring slots before this item, q buffers, blocks and units of this warp
+      bool ok = true;
+      for (int n = 0; ok && next_item(n, it); ++n) {
+        const int nb = it.u[t].nblk, klen = it.u[t].klen;
+        const int all = it.shared ? max(it.u[0].nblk, it.u[1].nblk) : nb;  // blocks of the stream
+        const int used = item_slots(it);
+        if (used == 0) continue;
+        const int qb = qn % C::qbufs;
+        // the keys that any token of the tile sees
+        const int seen = min(klen, it.u[t].lim0 + it.u[t].ntok - 1);
+        auto slot = [&](int e) { return g0 + slot_of(it, t, e); };
+        auto full = [&](int gs) { return tc::mbar_wait(kv_full + gs % C::slots, (gs / C::slots) & 1, status, 54, abort); };
+        auto release = [&](int gs) {  // the slot's reads are those of the instructions issued so far
+          tc::mma_commit(kv_empty + gs % C::slots);
+          if (!it.shared) tc::mma_commit(kv_empty + gs % C::slots);
+        };
+        auto issue_s = [&](int j) {
+          const int gs = slot(k_elem(j));
+          if (!full(gs)) return false;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            const uint32_t qa = tc::smem_u32(smem + C::q + (qb * 2 + t) * QA * kAtom);
+            const uint32_t ka = tc::smem_u32(smem + C::kv + (gs % C::slots) * C::slot);
+            for (int kk = 0; kk < qk_steps; ++kk)
+              tc::mma_f16(tS, tc::sw128_kmajor_desc(qa + (kk / 4) * kAtom + (kk % 4) * 32),
+                          tc::sw128_kmajor_desc(ka + (kk / 4) * kAtom + (kk % 4) * 32), id_s, kk != 0);
+            tc::mma_commit(s_full + t);
+            release(gs);
+            if (j == nb - 1) tc::mma_commit(q_empty + qb);
+          }
+          __syncwarp();
+          return true;
+        };
+        if (!tc::mbar_wait(q_full + qb, (qn / C::qbufs) & 1, status, 55, abort)) { ok = false; break; }
+        if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qb);
+        for (int j = 0; j < nb; ++j, ++blk) {
+          if (C::overlay || j == 0) {
+            // S_t is free once the softmax has read it; with P_t on top, once P_t * V has ended
+            if (blk > 0 && !tc::mbar_wait((C::overlay ? pv_done : s_free) + t, (blk - 1) & 1, status, 56, abort)) { ok = false; break; }
+            if (!issue_s(j)) { ok = false; break; }
+          }
+          if (!C::overlay && j + 1 < nb) {  // the next block's scores under this block's exponentials
+            if (!tc::mbar_wait(s_free + t, blk & 1, status, 57, abort) || !issue_s(j + 1)) { ok = false; break; }
+          }
+          const int gs = slot(v_elem(j, all));
+          if (!full(gs)) { ok = false; break; }
+          uint8_t *vs = smem + C::kv + (gs % C::slots) * C::slot;
+          const int live = min(kKeys, klen - j * kKeys);          // the sequence's rows of this block
+          const int steps = (min(kKeys, seen - j * kKeys) + 15) / 16;  // 16-key steps that some token sees
+          if (live < 16 * steps) {
+            // rows of no sequence: zeros, whatever they hold (both units of a pair write the same zeros)
+            const int rows = 16 * steps - live;
+            for (int c = lane; c < rows * 8 * VA; c += 32)
+              *reinterpret_cast<uint4 *>(vs + (c / (rows * 8)) * kAtom + (live + (c / 8) % rows) * 128 + (c % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            tc::fence_proxy_async();
+            __syncwarp();
+          }
+          if (!tc::mbar_wait(p_full + t, blk & 1, status, 58, abort) ||
+              (j == 0 && !tc::mbar_wait(o_free + t, (units & 1) ^ 1, status, 59, abort))) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          if (lane == 0) {
+            const uint32_t va = tc::smem_u32(vs);
+            for (int kk = 0; kk < steps; ++kk)
+              mma_ts(tO, tP + 8 * kk, v_desc(va + kk * 2048), id_pv, j != 0 || kk != 0);
+            tc::mma_commit(pv_done + t);
+            release(gs);
+          }
+          __syncwarp();
+        }
+        // a pair's first tile leaves the blocks that only the second sees, as they arrive
+        for (int j = nb; ok && j < all; ++j) {
+          for (int e : {k_elem(j), v_elem(j, all)}) {
+            const int gs = slot(e);
+            if (!full(gs)) { ok = false; break; }
+            if (lane == 0) tc::mbar_arrive(kv_empty + gs % C::slots);
+          }
+        }
+        g0 += used;
+        ++qn;
+        units += nb > 0;
+      }
+      if (lane == 0) tc::mma_commit(done);
+      tc::mbar_wait(done, 0, status, 60, abort);
+      if (*abort && lane == 0) drain(done, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---------------- softmax and output of unit t: row r of the tile
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int tok = r / a.G, head = r - tok * a.G;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + kOCol + kOStep * t + lane_off;
+    const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t + lane_off;
+    const float c = a.scale_log2;
+    int blk = 0;
+    Item it;
+    for (int n = 0; next_item(n, it); ++n) {
+      const int nb = it.u[t].nblk;
+      const bool row = tok < it.u[t].ntok && r < a.TQ * a.G;
+      const bool live = __any_sync(0xffffffffu, row);  // a warp without rows only keeps the barriers going
+      const int vis = row ? max(0, min(it.u[t].klen, it.u[t].lim0 + tok)) : 0;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nb; ++j, ++blk) {
+        if (!tc::mbar_wait(s_full + t, blk & 1, status, 61, abort)) { ok = false; break; }
+        tc::tc_fence_after();
+        if (!live) {
+          // its arrival for this block must not count for the one before: that block's P * V has ended
+          if (!C::overlay && lane == 0) tc::mbar_arrive(s_free + t);
+          if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 62, abort)) { ok = false; break; }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(p_full + t);
+          continue;
+        }
+        float sv[kKeys];
+        {
+          uint32_t raw[kKeys];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(tS + i, raw + i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 32) tmem_landed(raw + i);
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) sv[i] = __uint_as_float(raw[i]);
+        }
+        tc::tc_fence_before();
+        if (!C::overlay) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(s_free + t);
+        }
+        const int hi = vis - j * kKeys;
+        if (__any_sync(0xffffffffu, hi < kKeys)) {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (i >= hi) sv[i] = -INFINITY;
+        }
+        const float bm = row_max(sv);
+        bool need = false;
+        float alpha = 1.f;
+        if (j == 0) {
+          m = bm;
+        } else {
+          need = (bm - m) * c > kRescaleLog2;  // also from -inf, whose l and O are zero
+          if (need) {
+            alpha = ex2((m - bm) * c);
+            l *= alpha;
+            m = bm;
+          }
+        }
+        // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
+        const float negm = m == -INFINITY ? 0.f : -m * c;
+        const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
+        uint32_t pk[kKeys / 2];
+        float2 sum[4] = {};
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 d = __ffma2_rn(make_float2(sv[i + 2 * u], sv[i + 2 * u + 1]), c2, n2);
+            const float2 p = make_float2(ex2(d.x), ex2(d.y));
+            sum[u] = __fadd2_rn(sum[u], p);
+            pk[(i >> 1) + u] = pack2<kBF>(p.x, p.y);
+          }
+        }
+        const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+        l += s4.x + s4.y;
+        // P_t and O_t are free once the previous block's P * V has ended (with P_t over S_t this
+        // block's scores were only issued then)
+        if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 62, abort)) { ok = false; break; }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; i += 4) tmem_st4(tP + i, pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
+        tmem_wait_st();
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int i = 0; i < 64 * VA; i += 32) {
+            float v[32];
+            tc::tmem_ld32(tO + i, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= alpha;
+            tc::tmem_st32(tO + i, v);
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + t);
+      }
+      if (!ok) break;
+      if (nb > 0) {
+        if (!tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 63, abort)) break;
+        tc::tc_fence_after();
+      }
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that saw no key: zeros
+      const long long at = (long long)it.u[t].q_row + tok;
+      const int h = it.u[t].kvh * a.G + head;
+#pragma unroll
+      for (int i = 0; i < 64 * VA; i += 32) {
+        if (!live || i >= a.v_width) break;
+        float v[32];
+        if (nb > 0) tc::tmem_ld32(tO + i, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = inv == 0.f ? 0.f : v[k] * inv;
+        if (row && a.splits > 1) {
+          float *o = a.part + (((long long)it.u[t].split * a.q_rows + at) * a.heads + h) * a.v_width + i;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            if (i + k < a.v_width) *reinterpret_cast<float4 *>(o + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else if (row) {
+          uint16_t *o = static_cast<uint16_t *>(a.out) + at * a.out_token_stride + h * a.out_head_stride + i;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            if (i + k < a.v_width)
+              *reinterpret_cast<uint4 *>(o + k) = make_uint4(pack2<kBF>(v[k], v[k + 1]), pack2<kBF>(v[k + 2], v[k + 3]),
+                                                             pack2<kBF>(v[k + 4], v[k + 5]), pack2<kBF>(v[k + 6], v[k + 7]));
+        }
+        __syncwarp();
+      }
+      if (nb > 0) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(o_free + t);
+      }
+      if (row) {
+        if (a.splits > 1)
+          a.part_lse[((long long)it.u[t].split * a.q_rows + at) * a.heads + h] = l > 0.f || l != l ? m * c + log2f(l) : -INFINITY;
+        else if (a.lse)
+          a.lse[at * a.heads + h] = l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the key ranges: one warp per (query row, head); weights 2^(L_s - max L) of the ranges' log2
+// sums, in the order of the ranges.
+template <bool kBF>
+__global__ void __launch_bounds__(128) combine_kernel(const Args a) {
+  tc::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long n = (long long)a.q_rows * a.heads;
+  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < n; i += gridDim.x * 4ll) {
+    const long long tok = i / a.heads;
+    int lo = 0, hi = a.seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.q_offsets[mid] <= tok) lo = mid;
+      else hi = mid;
+    }
+    const Seq s = load_seq(a, lo);
+    if (tok < s.q0 || tok >= s.q0 + s.nq) continue;  // a row of no sequence
+    float top = -INFINITY;
+    for (int k = 0; k < a.splits; ++k) top = fmaxf(top, a.part_lse[k * n + i]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+    for (int k = 0; k < a.splits; ++k) {
+      const float ls = a.part_lse[k * n + i];
+      if (ls == -INFINITY) continue;
+      const float w = ex2(ls - top);
+      total += w;
+      if (4 * lane < a.v_width) {
+        const float4 p = *reinterpret_cast<const float4 *>(a.part + (k * n + i) * a.v_width + 4 * lane);
+        o.x = fmaf(w, p.x, o.x);
+        o.y = fmaf(w, p.y, o.y);
+        o.z = fmaf(w, p.z, o.z);
+        o.w = fmaf(w, p.w, o.w);
+      }
+    }
+    const bool any = total > 0.f || total != total;
+    const float inv = any ? 1.f / total : 0.f;
+    const long long h = i - tok * a.heads;
+    if (4 * lane < a.v_width)
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + tok * a.out_token_stride + h * a.out_head_stride + 4 * lane) =
+          make_uint2(pack2<kBF>(o.x * inv, o.y * inv), pack2<kBF>(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[i] = any ? (top + log2f(total)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+template <bool kBF, int QA, int VA>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
+  auto *k = attn_packed_kernel<kBF, QA, VA>;
+  const int smem = Cfg<QA, VA>::total + 1024;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, k);
+  if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorLaunchOutOfResources;  // the register split would wait for good
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k<<<grid, kThreads, smem, st>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
+}
+
+// Key ranges a tile is split into (even, or 1): enough for two units on every SM when there are few
+// tiles, each range at least two key blocks.
+int split_count(const mrf_attention_args &a) {
+  const int G = a.heads / a.kv_heads, TQ = kRows / G;
+  const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ);
+  const long long units = tiles * a.kv_heads, sms = sm_count();
+  const long long blocks = ((a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows) + kKeys - 1) / kKeys;
+  if (units > sms || blocks < 8) return 1;
+  const long long s = std::min<long long>({2 * (sms / units), blocks / 2, 128});
+  return s < 2 ? 1 : (int)(s & ~1ll);
+}
+
+bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
+
+}  // namespace
+
+bool attention_tc_takes(const mrf_attention_args &a) {
+  if (a.dtype != MRF_DTYPE_F16 && a.dtype != MRF_DTYPE_BF16) return false;
+  if (a.width > 128 || a.v_width > 128 || a.width % 8 || a.v_width % 8 || a.heads / a.kv_heads > kRows) return false;
+  const long long big = INT32_MAX - 65536;
+  if (a.k_rows < 1 || a.k_rows > big || a.q_rows * a.heads > big || (a.q_rows + a.seqs) * (long long)a.kv_heads * 64 > big) return false;
+  for (const void *p : {a.q, a.k, a.v, (const void *)a.out})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  return mult8(a.q_rows, a.q_token_stride) && mult8(a.heads, a.q_head_stride) && mult8(a.k_rows, a.k_token_stride) &&
+         mult8(a.kv_heads, a.k_head_stride) && mult8(a.k_rows, a.v_token_stride) && mult8(a.kv_heads, a.v_head_stride) &&
+         mult8(a.q_rows, a.out_token_stride) && mult8(a.heads, a.out_head_stride);
+}
+
+size_t attention_tc_workspace(const mrf_attention_args &a) {
+  const int s = split_count(a);
+  return s > 1 ? (size_t)s * a.q_rows * a.heads * (a.v_width + 1) * sizeof(float) : 0;
+}
+
+bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cudaError_t *err) {
+  Args a;
+  a.out = m.out;
+  a.lse = m.lse;
+  a.q_offsets = m.q_offsets;
+  a.k_start = m.k_start;
+  a.k_len = m.k_len;
+  a.out_token_stride = m.out_token_stride;
+  a.out_head_stride = m.out_head_stride;
+  a.q_rows = (int)m.q_rows;
+  a.k_rows = (int)m.k_rows;
+  a.seqs = m.seqs;
+  a.heads = m.heads;
+  a.kv_heads = m.kv_heads;
+  a.G = m.heads / m.kv_heads;
+  a.TQ = kRows / a.G;
+  a.width = m.width;
+  a.v_width = m.v_width;
+  a.causal = m.causal != 0;
+  a.splits = split_count(m);
+  a.scale = m.scale;
+  a.scale_log2 = m.scale * 1.4426950408889634f;
+  a.part = static_cast<float *>(m.workspace);
+  a.part_lse = a.part + (size_t)a.splits * a.q_rows * a.heads * a.v_width;
+
+  // a dimension of one row needs no stride; the maps want a valid one
+  auto st1 = [](long long n, long long s, int inner) { return (unsigned long long)(n <= 1 ? (inner + 7) / 8 * 8 : s); };
+  using ull = unsigned long long;
+  const ull qs_h = st1(m.heads, m.q_head_stride, m.width), qs_t = st1(m.q_rows, m.q_token_stride, m.width);
+  const ull qd[4] = {(ull)m.width, (ull)a.G, (ull)m.kv_heads, (ull)m.q_rows}, qst[3] = {qs_h, qs_h * a.G, qs_t};
+  const ull kd[3] = {(ull)m.width, (ull)m.kv_heads, (ull)m.k_rows};
+  const ull kst[2] = {st1(m.kv_heads, m.k_head_stride, m.width), st1(m.k_rows, m.k_token_stride, m.width)};
+  const ull vd[3] = {(ull)m.v_width, (ull)m.kv_heads, (ull)m.k_rows};
+  const ull vst[2] = {st1(m.kv_heads, m.v_head_stride, m.v_width), st1(m.k_rows, m.v_token_stride, m.v_width)};
+  const unsigned qbox[4] = {64, (unsigned)a.G, 1, (unsigned)a.TQ}, kbox[3] = {64, 1, kKeys};
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap(&tq, m.q, kTmF16, 4, qd, qst, qbox, 128) || !make_tmap(&tk, m.k, kTmF16, 3, kd, kst, kbox, 128) ||
+      !make_tmap(&tv, m.v, kTmF16, 3, vd, vst, kbox, 128))
+    return false;
+  const long long tiles = (m.q_rows + a.TQ - 1) / a.TQ + m.seqs;
+  const int grid = (int)std::min<long long>(tiles * m.kv_heads * std::max(1, a.splits / 2), sm_count());
+  const bool bf = m.dtype == MRF_DTYPE_BF16, q2 = m.width > 64, v2 = m.v_width > 64;
+#define MRF_ATTN(BF)                                                                                         \
+  (q2 ? (v2 ? launch<BF, 2, 2>(tq, tk, tv, a, grid, st) : launch<BF, 2, 1>(tq, tk, tv, a, grid, st))         \
+      : (v2 ? launch<BF, 1, 2>(tq, tk, tv, a, grid, st) : launch<BF, 1, 1>(tq, tk, tv, a, grid, st)))
+  *err = bf ? MRF_ATTN(true) : MRF_ATTN(false);
+#undef MRF_ATTN
+  if (*err != cudaSuccess || a.splits == 1) return true;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>((m.q_rows * m.heads + 3) / 4, 148 * 16));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  *err = bf ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a);
+  return true;
+}
+
+cudaError_t attention_tc_status(unsigned *word, cudaStream_t st) {
+  unsigned w[2] = {0, 0};
+  cudaError_t e = cudaMemcpyFromSymbolAsync(w, g_status, sizeof w, 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && w[0] != 0) {
+    const unsigned zero[2] = {0, 0};
+    e = cudaMemcpyToSymbolAsync(g_status, zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
+  word[0] = w[0];
+  word[1] = w[1];
+  return e;
+}
+
+}  // namespace mrf

@@ -175,17 +175,30 @@ mrf_status check_attention(const mrf_attention_args *a) {
 mrf_status mrf_attention_workspace(const mrf_attention_args *a, size_t *bytes) {
   if (!bytes) return op_fail(MRF_EINVAL, "mrf_attention_workspace: null bytes pointer");
   *bytes = 0;
-  return check_attention(a);
+  const mrf_status s = check_attention(a);
+  if (s == MRF_OK && a->q_rows > 0 && a->seqs > 0 && attention_tc_takes(*a)) *bytes = attention_tc_workspace(*a);
+  return s;
 }
 
 mrf_status mrf_attention(const mrf_attention_args *a, void *stream) {
   const mrf_status s = check_attention(a);
   if (s != MRF_OK || a->q_rows == 0 || a->seqs == 0) return s;
-  return op_done(launch_attention_rows(*a, static_cast<cudaStream_t>(stream)), "mrf_attention");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (attention_tc_takes(*a)) {
+    const size_t need = attention_tc_workspace(*a);
+    if (need > 0 && (!a->workspace || addr(a->workspace) % 16 || a->workspace_bytes < need))
+      return op_fail(MRF_EINVAL, "mrf_attention: the workspace must hold %zu bytes, 16-byte aligned", need);
+    cudaError_t e = cudaSuccess;
+    if (launch_attention_packed_tc(*a, st, &e)) return op_done(e, "mrf_attention");
+  }
+  return op_done(launch_attention_rows(*a, st), "mrf_attention");
 }
 
 mrf_status mrf_ops_sync_status(void *stream) {
-  return op_done(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)), "mrf_ops_sync_status");
+  unsigned word[2] = {0, 0};
+  const mrf_status s = op_done(attention_tc_status(word, static_cast<cudaStream_t>(stream)), "mrf_ops_sync_status");
+  if (s != MRF_OK || word[0] == 0) return s;
+  return op_fail(MRF_ETIMEOUT, "mrf_attention: a bounded wait expired on the device (site %u)", word[1]);
 }
 
 }  // extern "C"
