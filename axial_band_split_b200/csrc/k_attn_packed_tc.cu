@@ -28,6 +28,7 @@
 // by -inf whatever they are, and their rows of v, whose product with a zero probability could still
 // be NaN, are zeroed in shared memory before the second product.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "block_ops.h"
@@ -700,26 +701,40 @@ __global__ void __launch_bounds__(128) combine_kernel(const Args a) {
   }
 }
 
+int current_device() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev;
+}
+
 template <bool kBF, int QA, int VA>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
   auto *k = attn_packed_kernel<kBF, QA, VA>;
   const int smem = Cfg<QA, VA>::total + 1024;
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, k);
-  if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorLaunchOutOfResources;  // the register split would wait for good
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> ready{0};  // devices whose limits are set
+  const int dev = current_device();
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, k);
+    if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorLaunchOutOfResources;  // the register split would wait for good
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
   k<<<grid, kThreads, smem, st>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 
 int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
+  static std::atomic<int> known[64];
+  const int dev = current_device();
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
     cudaGetLastError();
-    n = 148;
+    return 148;
   }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

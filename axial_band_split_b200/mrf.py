@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import numpy as np
@@ -148,15 +149,15 @@ def lib():
         IP = ctypes.POINTER(I)
         L.mrf_chunk_plan.argtypes = [I, I, I, IP, IP, IP, IP, P, P, P, I]
         L.mrf_chunk_plan.restype = I
-        L.mrf_rms_norm.argtypes = [ctypes.POINTER(mrf_rms_norm_args), P]
+        L.mrf_rms_norm.argtypes = [P, P]
         L.mrf_rms_norm.restype = I
         L.mrf_rope_table.argtypes = [ctypes.POINTER(mrf_rope_config), P, ctypes.POINTER(ctypes.c_float)]
         L.mrf_rope_table.restype = I
-        L.mrf_rope.argtypes = [ctypes.POINTER(mrf_rope_args), P]
+        L.mrf_rope.argtypes = [P, P]
         L.mrf_rope.restype = I
-        L.mrf_attention_workspace.argtypes = [ctypes.POINTER(mrf_attention_args), ctypes.POINTER(ctypes.c_size_t)]
+        L.mrf_attention_workspace.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
         L.mrf_attention_workspace.restype = I
-        L.mrf_attention.argtypes = [ctypes.POINTER(mrf_attention_args), P]
+        L.mrf_attention.argtypes = [P, P]
         L.mrf_attention.restype = I
         L.mrf_ops_sync_status.argtypes = [P]
         L.mrf_ops_sync_status.restype = I
@@ -223,53 +224,103 @@ def _stream_ptr(stream):
 
 
 # ------------------------------------------------------------------ block operators
-def _require(ok, message, status=-1):
-    if not ok:
-        raise MrfError(status, message)
+# A call of these takes microseconds on the device, so the binding keeps its own share small: checks
+# build no message unless they fail, and the argument structures (the ctypes classes above, laid out
+# the same) are packed in one go.
+_NORM = struct.Struct("6P5q6if0P")
+_ROPE = struct.Struct("6P9q7if0P")
+_ATTENTION = struct.Struct("9PN11q7if0P")
 
 
-def _dtype(x, name):
-    """mrf_dtype of a CUDA tensor of one of the block operators' types; they compute no gradients."""
-    import torch
-    _require(isinstance(x, torch.Tensor) and x.is_cuda, f"{name} must be a CUDA tensor")
-    _require(not (x.requires_grad and torch.is_grad_enabled()), f"{name} requires a gradient; the library is for inference")
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(x.dtype)
-    _require(code is not None, f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+class _Torch:
+    """What the block operators use of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        self.e4m3, self.f32, self.i32, self.i64, self.u8 = (torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64,
+                                                            torch.uint8)
+        self.empty_like = torch.empty_like  # keeps the order of the strides, so that is where outputs' strides come from
+        self.grad, self.device, self.Tensor = torch.is_grad_enabled, torch.cuda.current_device, torch.Tensor
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _code(t, x, name, dev=None):
+    """mrf_dtype of a CUDA tensor (on device `dev`) of one of the block operators' types; they compute no gradients."""
+    if not isinstance(x, t.Tensor):
+        raise MrfError(-1, f"{name} must be a tensor, got {type(x).__name__}")
+    code = t.codes.get(x.dtype)
+    if code is None:
+        raise MrfError(-1, f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    at = x.get_device()
+    if at < 0 or (dev is not None and at != dev):
+        raise MrfError(-1, f"{name} must be on {'a CUDA device' if dev is None else f'cuda:{dev}'}, is on {x.device}")
+    if x.requires_grad and t.grad():
+        raise MrfError(-1, f"{name} requires a gradient; the library is for inference")
     return code
 
 
-def _match(x, like, name, shape):
-    """`x` has like's type and device and the given shape, its last dimension contiguous."""
-    _require(x.is_cuda and x.device == like.device, f"{name} must be on {like.device}")
-    _require(x.dtype == like.dtype, f"{name} must be {like.dtype}, got {x.dtype}")
-    _require(tuple(x.shape) == tuple(shape), f"{name} must be {tuple(shape)}, got {tuple(x.shape)}", -2)
-    _require(x.shape[-1] <= 1 or x.stride(-1) == 1, f"{name}: the last dimension must be contiguous")
+def _like(x, dtype, dev, shape, name):
+    """`x` is a tensor of the given type, device and shape, its last dimension contiguous; its strides."""
+    if x.dtype != dtype or x.get_device() != dev:
+        raise MrfError(-1, f"{name} must be {dtype} on cuda:{dev}, is {x.dtype} on {x.device}")
+    if x.shape != shape:
+        raise MrfError(-2, f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
+    st = x.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise MrfError(-1, f"{name}: the last dimension must be contiguous")
+    return st
 
 
-def _index(x, like, name, count, wide=False):
-    """`x` is a contiguous int32 (or int64 where `wide`) vector of `count` values on like's device."""
-    import torch
-    _require(isinstance(x, torch.Tensor) and x.is_cuda and x.device == like.device, f"{name} must be on {like.device}")
-    _require(x.dtype == torch.int32 or (wide and x.dtype == torch.int64),
-             f"{name} must be int32{' or int64' if wide else ''}, got {x.dtype}")
-    _require(x.dim() == 1 and x.shape[0] == count and (count <= 1 or x.stride(0) == 1),
-             f"{name} must be a contiguous vector of {count} values", -2)
+def _vector(t, x, dev, count, name, wide=False):
+    """`x` is a contiguous int32 (or int64 where `wide`) vector of `count` values on device `dev`."""
+    if not isinstance(x, t.Tensor) or x.get_device() != dev or not (x.dtype == t.i32 or (wide and x.dtype == t.i64)):
+        raise MrfError(-1, f"{name} must be an int32{' or int64' if wide else ''} tensor on cuda:{dev}")
+    if x.dim() != 1 or x.shape[0] != count or (count > 1 and x.stride(0) != 1):
+        raise MrfError(-2, f"{name} must be a contiguous vector of {count} values, got {tuple(x.shape)}")
 
 
-def _on_device(call, x, stream):
-    """call(stream pointer) with x's device current and `stream` (a torch stream or a pointer; None: the
-    current one) as torch's current stream, so that what the call allocates belongs to it."""
-    import torch
-    if stream is None and x.device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(x.device):
-        if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=x.device)
-        _require(stream.device == x.device, f"the stream must be on {x.device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+def _row_stride(x, st, dim, name):
+    """The row stride of a [rows, dim] tensor, or of one with other leading dimensions (contiguous)."""
+    if len(st) == 2:
+        return st[0]
+    if not x.is_contiguous():
+        raise MrfError(-1, f"{name} with other than two dimensions must be contiguous")
+    return dim
+
+
+class _scope:
+    """Device `dev` and `stream` (a torch stream, a pointer, or None for dev's current one) made torch's
+    current ones, so that what a call allocates belongs to the stream it runs on."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self.on = [torch.cuda.device(dev)]
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", dev))
+            if stream.device.index != dev:
+                raise MrfError(-1, f"the stream must be on cuda:{dev}, is on {stream.device}")
+            self.on.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.on:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.on):
+            c.__exit__(*e)
 
 
 class RmsNorm(NamedTuple):
@@ -285,59 +336,56 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None, group=0, c
     """mrf_rms_norm: h = x + residual, then h * weight / sqrt(mean h^2 + eps) over the last dimension
     (with clamp: h * weight / max(sqrt(mean h^2), eps)).
 
-    x: CUDA float32, float16 or bfloat16 [rows, dim] (any row stride), or contiguous with more leading
+    x: CUDA float32, float16 or bfloat16 [rows, dim] (any row stride), or contiguous with other leading
     dimensions; residual the same; weight [dim] of any of the three types.  out_dtype
     torch.float8_e4m3fn gives 8-bit rows and float32 scales [..., ceil(dim / group)], one for each
     `group` columns (0: the row), out * scale standing for the value.  out=x norms in place,
     residual_out=residual updates the residual in place; without residual_out h gets a new tensor.
     Returns RmsNorm(out, scales, residual)."""
-    import torch
-    code = _dtype(x, "x")
-    _require(x.dim() >= 1 and x.shape[-1] >= 1, "x must have a last dimension of at least 1", -2)
-    quant = out_dtype == torch.float8_e4m3fn
-    _require(quant or out_dtype is None or out_dtype == x.dtype, "out_dtype must be x's type or torch.float8_e4m3fn")
-    dim = x.shape[-1]
-    rows = x.numel() // dim
-
-    def stride(t, name):
-        _require(t.dim() == 2 or t.is_contiguous(), f"{name} with more than two dimensions must be contiguous")
-        return t.stride(0) if t.dim() == 2 else dim
-
-    _match(x, x, "x", x.shape)
-    _require(residual is not None or residual_out is None, "residual_out without residual")
-    wcode = 0
+    t = _t()
+    code = _code(t, x, "x")
+    dev = x.get_device()
+    if stream is not None or dev != t.device():
+        with _scope(dev, stream):
+            return rms_norm(x, weight, eps, residual, out_dtype, group, clamp, out, residual_out)
+    shape = x.shape
+    if len(shape) == 0 or shape[-1] < 1:
+        raise MrfError(-2, "x must have a last dimension of at least 1")
+    dim, dtype = shape[-1], x.dtype
+    quant = out_dtype == t.e4m3
+    if not quant and out_dtype is not None and out_dtype != dtype:
+        raise MrfError(-1, f"out_dtype must be {dtype} or torch.float8_e4m3fn, got {out_dtype}")
+    x_row = _row_stride(x, _like(x, dtype, dev, shape, "x"), dim, "x")
+    w = wcode = res = res_row = res_out = res_out_row = scale_ptr = 0
     if weight is not None:
-        wcode = _dtype(weight, "weight")
-        _require(weight.device == x.device and tuple(weight.shape) == (dim,) and (dim == 1 or weight.stride(0) == 1),
-                 f"weight must be a contiguous [{dim}] on {x.device}", -2)
+        wcode = _code(t, weight, "weight", dev)
+        if weight.shape != (dim,) or (dim > 1 and weight.stride(0) != 1):
+            raise MrfError(-2, f"weight must be a contiguous vector of {dim} values, got {tuple(weight.shape)}")
+        w = weight.data_ptr()
+    h, scales = residual_out, None
     if residual is not None:
-        _dtype(residual, "residual")
-        _match(residual, x, "residual", x.shape)
-
-    def call(st):
-        o = torch.empty(x.shape, dtype=torch.float8_e4m3fn if quant else x.dtype, device=x.device) if out is None else out
-        if out is not None:
-            _require(o.dtype == (torch.float8_e4m3fn if quant else x.dtype), f"out has the wrong type, {o.dtype}")
-            _match(o, o, "out", x.shape)
-            _require(o.device == x.device, f"out must be on {x.device}")
-        scales = torch.empty(x.shape[:-1] + (-(-dim // group) if group > 0 else 1,), dtype=torch.float32,
-                             device=x.device) if quant else None
-        h = residual_out
-        if residual is not None:
-            if h is None:
-                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            _match(h, x, "residual_out", x.shape)
-        a = mrf_rms_norm_args(
-            x.data_ptr(), residual.data_ptr() if residual is not None else None,
-            weight.data_ptr() if weight is not None else None, o.data_ptr(), h.data_ptr() if h is not None else None,
-            scales.data_ptr() if quant else None, rows, stride(x, "x"),
-            stride(residual, "residual") if residual is not None else 0, stride(o, "out"),
-            stride(h, "residual_out") if h is not None else 0, dim, code, wcode, 3 if quant else code, group,
-            int(clamp), eps)
-        _check(lib().mrf_rms_norm(ctypes.byref(a), st))
-        return RmsNorm(o, scales, h)
-
-    return _on_device(call, x, stream)
+        _code(t, residual, "residual", dev)
+        res_row = _row_stride(residual, _like(residual, dtype, dev, shape, "residual"), dim, "residual")
+        res = residual.data_ptr()
+        if h is None:
+            h, res_out_row = t.empty_like(x) if x.is_contiguous() else x.new_empty(shape), dim
+        else:
+            res_out_row = _row_stride(h, _like(h, dtype, dev, shape, "residual_out"), dim, "residual_out")
+        res_out = h.data_ptr()
+    elif h is not None:
+        raise MrfError(-1, "residual_out without residual")
+    if out is None:
+        kind = t.e4m3 if quant else dtype
+        out, out_row = t.empty_like(x, dtype=kind) if x.is_contiguous() else x.new_empty(shape, dtype=kind), dim
+    else:
+        out_row = _row_stride(out, _like(out, t.e4m3 if quant else dtype, dev, shape, "out"), dim, "out")
+    if quant:
+        scales = x.new_empty(shape[:-1] + (-(-dim // group) if group > 0 else 1,), dtype=t.f32)
+        scale_ptr = scales.data_ptr()
+    _check(lib().mrf_rms_norm(_NORM.pack(
+        x.data_ptr(), res, w, out.data_ptr(), res_out, scale_ptr, x.numel() // dim, x_row, res_row, out_row, res_out_row,
+        dim, code, wcode, 3 if quant else code, group, bool(clamp), eps), t.stream(dev)))
+    return RmsNorm(out, scales, h)
 
 
 class RopeTable(NamedTuple):
@@ -354,7 +402,8 @@ def rope_table(part, theta=10000.0, scaling="none", factor=1.0, original=0, beta
     training's context length).  Made once and kept; rope takes it."""
     import torch
     kinds = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-    _require(scaling in kinds, f"scaling must be one of {sorted(kinds)}, got {scaling!r}")
+    if scaling not in kinds:
+        raise MrfError(-1, f"scaling must be one of {sorted(kinds)}, got {scaling!r}")
     c = mrf_rope_config(part, kinds[scaling], theta, factor, original, beta_fast, beta_slow)
     turns = np.zeros(max(1, min(part, 1024) // 2), np.uint64)
     scale = ctypes.c_float(0)
@@ -367,40 +416,46 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     [tokens, kv_heads, width] (or None) turned by each token's position (int32 or int64 [tokens]), in pairs
     (2i, 2i + 1), or (i, i + part / 2) with interleaved=False.  Heads and tokens may have any strides
     (column ranges of a projection's rows); q_out=q and k_out=k turn in place.  Returns (q_out, k_out)."""
-    import torch
-    code = _dtype(q, "q")
-    _require(q.dim() == 3, f"q must be [tokens, heads, width], got {tuple(q.shape)}", -2)
-    _match(q, q, "q", q.shape)
-    tokens, heads, width = q.shape
-    kv_heads = 0
+    t = _t()
+    code = _code(t, q, "q")
+    dev = q.get_device()
+    if stream is not None or dev != t.device():
+        with _scope(dev, stream):
+            return rope(q, k, positions, table, interleaved, q_out, k_out)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise MrfError(-2, f"q must be [tokens, heads, width], got {tuple(shape)}")
+    tokens, heads, width = shape
+    qs = _like(q, dtype, dev, shape, "q")
+    ks = kos = (0, 0, 1)
+    kv_heads = k_ptr = k_out_ptr = 0
     if k is not None:
-        _dtype(k, "k")
-        _require(k.dim() == 3, f"k must be [tokens, kv_heads, width], got {tuple(k.shape)}", -2)
+        _code(t, k, "k", dev)
+        if k.dim() != 3:
+            raise MrfError(-2, f"k must be [tokens, kv_heads, width], got {tuple(k.shape)}")
         kv_heads = k.shape[1]
-        _match(k, q, "k", (tokens, kv_heads, width))
-    _require(k is not None or k_out is None, "k_out without k")
-    _index(positions, q, "positions", tokens, wide=True)
-    _require(isinstance(table, RopeTable), "table must come from rope_table")
-    _require(table.turns.device == q.device, f"the table must be on {q.device}")
-
-    def call(st):
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _match(qo, q, "q_out", q.shape)
-        ko = k_out
-        if k is not None:
-            if ko is None:
-                ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            _match(ko, k, "k_out", k.shape)
-        a = mrf_rope_args(
-            q.data_ptr(), k.data_ptr() if kv_heads else None, qo.data_ptr(), ko.data_ptr() if kv_heads else None,
-            positions.data_ptr(), table.turns.data_ptr(), tokens, q.stride(0), q.stride(1),
-            k.stride(0) if kv_heads else 0, k.stride(1) if kv_heads else 0, qo.stride(0), qo.stride(1),
-            ko.stride(0) if kv_heads else 0, ko.stride(1) if kv_heads else 0, heads, kv_heads, width, table.part, code,
-            int(positions.dtype == torch.int64), int(interleaved), table.scale)
-        _check(lib().mrf_rope(ctypes.byref(a), st))
-        return qo, ko
-
-    return _on_device(call, q, stream)
+        ks = _like(k, dtype, dev, (tokens, kv_heads, width), "k")
+        if k_out is None:
+            k_out = t.empty_like(k)
+            kos = k_out.stride()
+        else:
+            kos = _like(k_out, dtype, dev, (tokens, kv_heads, width), "k_out")
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise MrfError(-1, "k_out without k")
+    _vector(t, positions, dev, tokens, "positions", wide=True)
+    if not isinstance(table, RopeTable) or table.turns.get_device() != dev:
+        raise MrfError(-1, f"table must come from rope_table on cuda:{dev}")
+    if q_out is None:
+        q_out = t.empty_like(q)
+        qos = q_out.stride()
+    else:
+        qos = _like(q_out, dtype, dev, shape, "q_out")
+    _check(lib().mrf_rope(_ROPE.pack(
+        q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(), table.turns.data_ptr(), tokens, qs[0], qs[1],
+        ks[0], ks[1], qos[0], qos[1], kos[0], kos[1], heads, kv_heads, width, table.part, code, positions.dtype == t.i64,
+        bool(interleaved), table.scale), t.stream(dev)))
+    return q_out, k_out
 
 
 def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, causal=True, scale=None, out=None,
@@ -414,45 +469,55 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
     bound of the key counts known on the host (0: k's rows), which only decides how the work is split.
     Rows of no sequence keep what `out` held (a new `out` is uninitialised there).  Returns out
     [q_rows, heads, v_width], or (out, lse float32 [q_rows, heads]) with return_lse."""
-    import torch
-    code = _dtype(q, "q")
-    _require(q.dim() == 3, f"q must be [q_rows, heads, width], got {tuple(q.shape)}", -2)
-    _dtype(k, "k")
-    _dtype(v, "v")
-    _require(k.dim() == 3 and v.dim() == 3, "k and v must be [k_rows, kv_heads, width]", -2)
-    q_rows, heads, width = q.shape
-    k_rows, kv_heads, v_width = v.shape
-    _match(q, q, "q", q.shape)
-    _match(k, q, "k", (k_rows, kv_heads, width))
-    _match(v, q, "v", v.shape)
-    _require(isinstance(q_offsets, torch.Tensor) and q_offsets.dim() == 1 and q_offsets.shape[0] >= 1,
-             "q_offsets must be [seqs + 1]", -2)
+    t = _t()
+    code = _code(t, q, "q")
+    dev = q.get_device()
+    if stream is not None or dev != t.device():
+        with _scope(dev, stream):
+            return attention_packed(q, k, v, q_offsets, k_start, k_len, max_k, causal, scale, out, return_lse)
+    _code(t, k, "k", dev)
+    _code(t, v, "v", dev)
+    dtype, shape, v_shape = q.dtype, q.shape, v.shape
+    if len(shape) != 3 or len(v_shape) != 3:
+        raise MrfError(-2, f"q and v must be [rows, heads, width], got {tuple(shape)} and {tuple(v_shape)}")
+    q_rows, heads, width = shape
+    k_rows, kv_heads, v_width = v_shape
+    qs, ks, vs = (_like(q, dtype, dev, shape, "q"), _like(k, dtype, dev, (k_rows, kv_heads, width), "k"),
+                  _like(v, dtype, dev, v_shape, "v"))
+    if not isinstance(q_offsets, t.Tensor) or q_offsets.dim() != 1 or q_offsets.shape[0] < 1:
+        raise MrfError(-2, "q_offsets must be a vector of seqs + 1 values")
     seqs = q_offsets.shape[0] - 1
-    _index(q_offsets, q, "q_offsets", seqs + 1)
-    _require((k_start is None) == (k_len is None), "k_start and k_len go together")
+    _vector(t, q_offsets, dev, seqs + 1, "q_offsets")
+    if (k_start is None) != (k_len is None):
+        raise MrfError(-1, "k_start and k_len go together")
+    start_ptr = len_ptr = lse_ptr = 0
     if k_len is not None:
-        _index(k_start, q, "k_start", seqs)
-        _index(k_len, q, "k_len", seqs)
-
-    def call(st):
-        o = torch.empty((q_rows, heads, v_width), dtype=q.dtype, device=q.device) if out is None else out
-        _match(o, q, "out", (q_rows, heads, v_width))
-        lse = torch.empty((q_rows, heads), dtype=torch.float32, device=q.device) if return_lse else None
-        a = mrf_attention_args(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr() if return_lse else None,
-            q_offsets.data_ptr(), k_start.data_ptr() if k_len is not None else None,
-            k_len.data_ptr() if k_len is not None else None, None, 0, q_rows, k_rows, max_k, q.stride(0), q.stride(1),
-            k.stride(0), k.stride(1), v.stride(0), v.stride(1), o.stride(0), o.stride(1), seqs, heads, kv_heads, width,
-            v_width, code, int(causal), width ** -0.5 if scale is None else scale)
-        need = ctypes.c_size_t(0)
-        _check(lib().mrf_attention_workspace(ctypes.byref(a), ctypes.byref(need)))
-        if need.value:
-            space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-            a.workspace, a.workspace_bytes = space.data_ptr(), need.value
-        _check(lib().mrf_attention(ctypes.byref(a), st))
-        return (o, lse) if return_lse else o
-
-    return _on_device(call, q, stream)
+        _vector(t, k_start, dev, seqs, "k_start")
+        _vector(t, k_len, dev, seqs, "k_len")
+        # (a vector of no values has a null pointer; any other says that k_start and k_len are given)
+        start_ptr, len_ptr = (k_start.data_ptr(), k_len.data_ptr()) if seqs else (8, 8)
+    if out is None:
+        out = t.empty_like(q) if v_width == width else q.new_empty((q_rows, heads, v_width))
+        os_ = out.stride()
+    else:
+        os_ = _like(out, dtype, dev, (q_rows, heads, v_width), "out")
+    lse = None
+    if return_lse:
+        lse = q.new_empty((q_rows, heads), dtype=t.f32)
+        lse_ptr = lse.data_ptr()
+    L = lib()
+    args = [q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, q_offsets.data_ptr(), start_ptr, len_ptr, 0, 0,
+            q_rows, k_rows, max_k, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], seqs, heads, kv_heads, width, v_width,
+            code, bool(causal), width ** -0.5 if scale is None else scale]
+    packed = _ATTENTION.pack(*args)
+    need = ctypes.c_size_t()
+    _check(L.mrf_attention_workspace(packed, ctypes.byref(need)))
+    if need.value:
+        space = q.new_empty(need.value, dtype=t.u8)
+        args[8], args[9] = space.data_ptr(), need.value
+        packed = _ATTENTION.pack(*args)
+    _check(L.mrf_attention(packed, t.stream(dev)))
+    return (out, lse) if return_lse else out
 
 
 def ops_sync_status(stream=None):

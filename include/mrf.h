@@ -358,7 +358,8 @@ int mrf_launches_per_forward(const mrf_handle *h, int B, int T);
  * With out_dtype MRF_DTYPE_E4M3 the output is 8-bit: scales[r, g] = max |y| / 448 over each group
  * of `group` columns (0: the whole row; the last group may be short) of y = the formula above,
  * and out = y / scales[r, g] rounded to the nearest e4m3 (ties to even); a group of zeros has
- * scale 0 and codes 0, a row with a NaN or an infinity NaN scales and codes.
+ * scale 0 and codes 0; a NaN makes its whole row's scales and codes NaN, an infinity its group's (the rest
+ * of its row is 0).
  * out may be x, and residual_out may be residual (same pointer, stride and type); any other overlap is undefined.
  * Rows whose sum of squares passes the fp32 range are not supported (x beyond about 1e18).
  */

@@ -94,6 +94,12 @@ def test_attention_refusals(change, status):
     assert need.value == 0
 
 
+@pytest.mark.parametrize("packer,args", [(mrf._NORM, norm_args()), (mrf._ROPE, rope_args()), (mrf._ATTENTION, attention_args())])
+def test_packed_arguments_are_the_structures(packer, args):
+    values = [getattr(args, n) or 0 for n, _ in args._fields_]
+    assert packer.pack(*values) == bytes(args)
+
+
 def test_null_and_empty_calls():
     L = mrf.lib()
     assert L.mrf_rms_norm(None, None) == L.mrf_rope(None, None) == L.mrf_attention(None, None) == EINVAL
