@@ -7,8 +7,9 @@
 // registers, and one exchange between the warps serves both.
 //
 // Rows up to 512 wide take a warp each (no exchange between warps), wider ones a block; a thread
-// holds V vectors of 8 values.  What hides a row's load latency is the other rows on the SM, so the
-// register budget is 64 a thread (1024 threads an SM).
+// holds V vectors of 8 values.  The arithmetic, about 10 instructions a value with the conversions,
+// is the next bound: it runs on packed fp32 pairs, and the work that a row costs every thread (the
+// sums' exchange, the root, the scales) is spread over the thread's 16 values.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -17,8 +18,6 @@
 
 namespace mrf {
 namespace {
-
-constexpr int kMaxWarps = 16;
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // keeps a NaN
   float d;
@@ -31,11 +30,6 @@ __device__ __forceinline__ float warp_max(float v, int width) {
 }
 
 // 8 values of a row as they lie in memory.
-template <class T>
-struct Raw {
-  T v[8];
-};
-
 // Columns of value e of this lane's vector, whose warp's 256 columns begin at c0.  kVec: 8 neighbours
 // (16-byte accesses); else 32 apart, so that a warp's accesses of one value are neighbours.
 template <bool kVec>
@@ -43,67 +37,131 @@ __device__ __forceinline__ int column(int c0, int lane, int e) {
   return kVec ? c0 + 8 * lane + e : c0 + 32 * e + lane;
 }
 
+// Two 16-bit values as fp32, and back.
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t u);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
+  return __half22float2(*reinterpret_cast<__half2 *>(&u));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float2 f);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float2 f) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(f);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float2 f) {
+  const __half2 h = __float22half2_rn(f);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 8 values of a row as they lie in memory: zeros past its end.
 template <class T, bool kVec>
-__device__ __forceinline__ void load8(const T *row, int c0, int lane, int dim, Raw<T> &r) {
+struct Raw {
+  uint4 v[sizeof(T) / 2];  // kVec
+  T s[8];                  // else
+  __device__ __forceinline__ void load(const T *row, int c0, int lane, int dim) {
+    if constexpr (kVec) {
+      const int c = c0 + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        v[i] = c < dim ? reinterpret_cast<const uint4 *>(row + c)[i] : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<false>(c0, lane, e);
+        s[e] = c < dim ? row[c] : from_f32<T>(0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (!kVec) return make_float2(to_f32(s[2 * i]), to_f32(s[2 * i + 1]));
+    const uint4 u = v[sizeof(T) == 4 ? i / 2 : 0];
+    if constexpr (sizeof(T) == 4)
+      return i & 1 ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w)) : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    else
+      return unpack2<T>(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w);
+  }
+};
+
+template <class T, bool kVec>
+__device__ __forceinline__ void store8(T *row, int c0, int lane, int dim, const float2 (&f)[4]) {
   if constexpr (kVec) {
     const int c = c0 + 8 * lane;
-    if (c < dim) {
-      const uint4 *p = reinterpret_cast<const uint4 *>(row + c);
-      uint4 *q = reinterpret_cast<uint4 *>(r.v);
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = p[i];
+    if (c >= dim) return;
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4 *>(row + c)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      reinterpret_cast<float4 *>(row + c)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    } else {
+      *reinterpret_cast<uint4 *>(row + c) = make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (column<false>(c0, lane, e) < dim) r.v[e] = row[column<false>(c0, lane, e)];
+      if (column<false>(c0, lane, e) < dim) row[column<false>(c0, lane, e)] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
   }
 }
 
-template <class T, bool kVec>
-__device__ __forceinline__ void store8(T *row, int c0, int lane, int dim, const float (&f)[8]) {
-  if constexpr (kVec) {
-    const int c = c0 + 8 * lane;
-    if (c < dim) {
-      Raw<T> r;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(f[e]);
-      uint4 *p = reinterpret_cast<uint4 *>(row + c);
-      const uint4 *q = reinterpret_cast<const uint4 *>(r.v);
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) p[i] = q[i];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (column<false>(c0, lane, e) < dim) row[column<false>(c0, lane, e)] = from_f32<T>(f[e]);
-  }
-}
-
-// The weight's 8 values at this lane's columns.
+// f *= weight at this lane's columns.  wide: the weight is fp32 and 16-byte aligned.
 template <bool kVec>
-__device__ __forceinline__ void load_weight(const mrf_rms_norm_args &a, bool wide, int c0, int lane, float (&w)[8]) {
-  if (!a.weight) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 1.f;
-  } else if (kVec && wide) {
+__device__ __forceinline__ void times_weight(const mrf_rms_norm_args &a, bool wide, int c0, int lane, float2 (&f)[4]) {
+  if (!a.weight) return;
+  if (kVec && wide) {
+    if (c0 + 8 * lane >= a.dim) return;
     const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.weight) + c0 + 8 * lane);
-    const bool in = c0 + 8 * lane < a.dim;
-    const float4 u = in ? __ldg(p) : make_float4(0.f, 0.f, 0.f, 0.f), v = in ? __ldg(p + 1) : u;
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+    const float4 u = __ldg(p), v = __ldg(p + 1);
+    f[0] = __fmul2_rn(f[0], make_float2(u.x, u.y));
+    f[1] = __fmul2_rn(f[1], make_float2(u.z, u.w));
+    f[2] = __fmul2_rn(f[2], make_float2(v.x, v.y));
+    f[3] = __fmul2_rn(f[3], make_float2(v.z, v.w));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = column<kVec>(c0, lane, e);
-      w[e] = c < a.dim ? load_any(a.weight, a.weight_dtype, c) : 0.f;
+      float &x = e & 1 ? f[e / 2].y : f[e / 2].x;
+      if (c < a.dim) x *= load_any(a.weight, a.weight_dtype, c);
     }
   }
 }
 
-// kWarpRow: a warp a row; else a block a row.  wide: the weight is fp32 and 16-byte aligned.
+__device__ __forceinline__ float max8(float m, const float2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_nan(max_nan(m, fabsf(f[i].x)), fabsf(f[i].y));
+  return m;
+}
+
+// Asynchronous copies of a thread's own vectors into its own places in shared memory: nobody else
+// reads them, so the thread's own wait is all the ordering they need.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 load_shared(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+struct Plan {
+  bool wide;        // the weight is fp32 and 16-byte aligned
+  float inv_dim, inv_eps;
+  int log2_group;   // of a.group
+};
+
+// Any shape: kWarpRow: a warp a row; else a block a row.
 template <class T, int V, bool kWarpRow, bool kVec>
-__global__ void __launch_bounds__(32 * kMaxWarps, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf_rms_norm_args a, const bool wide) {
-  __shared__ float red[2][2][kMaxWarps];
+__global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf_rms_norm_args a, const Plan plan) {
+  __shared__ float red[2][2][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
   const bool quant = a.out_dtype == MRF_DTYPE_E4M3, row_scale = quant && a.group == 0;
@@ -111,39 +169,34 @@ __global__ void __launch_bounds__(32 * kMaxWarps, V <= 2 ? 2 : 1) rms_norm_kerne
   const long long step = kWarpRow ? gridDim.x * (long long)warps : gridDim.x;
   int buf = 0;
   for (long long r = kWarpRow ? blockIdx.x * (long long)warps + warp : blockIdx.x; r < a.rows; r += step, buf ^= 1) {
-    float h[V][8], ss = 0.f, top = 0.f;
-    Raw<T> xr[V], rr[V];
     auto first_column = [&](int v) { return 256 * (kWarpRow ? v : v * warps + warp); };
+    float2 h[V][4];
+    {
+      Raw<T, kVec> xr[V], rr[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xr[v].v[e] = rr[v].v[e] = from_f32<T>(0.f);
-      load8<T, kVec>(x + r * a.x_stride, first_column(v), lane, a.dim, xr[v]);
-      if (res) load8<T, kVec>(res + r * a.residual_stride, first_column(v), lane, a.dim, rr[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[v][e] = to_f32(xr[v].v[e]) + to_f32(rr[v].v[e]);
-        ss = fmaf(h[v][e], h[v][e], ss);
+      for (int v = 0; v < V; ++v) {
+        xr[v].load(x + r * a.x_stride, first_column(v), lane, a.dim);
+        if (res) rr[v].load(res + r * a.residual_stride, first_column(v), lane, a.dim);
       }
-      if (a.residual_out)
-        store8<T, kVec>(static_cast<T *>(a.residual_out) + r * a.residual_out_stride, first_column(v), lane, a.dim, h[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float w[8];
-      load_weight<kVec>(a, wide, first_column(v), lane, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] *= w[e];
-    }
-    // the row's sum of squares and, for one scale a row, its largest |h w|
-    if (row_scale) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(h[v][e]));
+        for (int i = 0; i < 4; ++i) h[v][i] = res ? __fadd2_rn(xr[v].pair(i), rr[v].pair(i)) : xr[v].pair(i);
+    }
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s2 = __ffma2_rn(h[v][i], h[v][i], s2);
+      if (a.residual_out)
+        store8<T, kVec>(static_cast<T *>(a.residual_out) + r * a.residual_out_stride, first_column(v), lane, a.dim, h[v]);
+      times_weight<kVec>(a, plan.wide, first_column(v), lane, h[v]);
+    }
+    // the row's sum of squares and, for one scale a row, its largest |h w|
+    float ss = s2.x + s2.y, top = 0.f;
+    if (row_scale) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) top = max8(top, h[v]);
       top = warp_max(top, 32);
     }
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -158,54 +211,50 @@ __global__ void __launch_bounds__(32 * kMaxWarps, V <= 2 ? 2 : 1) rms_norm_kerne
       if (row_scale)
         for (int i = 0; i < warps; ++i) top = max_nan(top, red[buf][1][i]);
     }
-    const float mean = ss / (float)a.dim;
-    const float s = a.clamp ? 1.f / fmaxf(sqrtf(mean), a.eps) : 1.f / sqrtf(mean + a.eps);
+    // clamp: 1 / max(sqrt(mean), eps) = min(1 / sqrt(mean), 1 / eps), a NaN kept
+    const float mean = ss * plan.inv_dim;
+    float s = a.clamp ? rsqrtf(mean) : rsqrtf(mean + a.eps);
+    if (a.clamp && s > plan.inv_eps) s = plan.inv_eps;
     if (!quant) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] *= s;
+        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(s, s));
         store8<T, kVec>(static_cast<T *>(a.out) + r * a.out_stride, first_column(v), lane, a.dim, h[v]);
       }
       continue;
     }
     // scale = s max |h w| / 448 over the group, code = h w * (448 / max |h w|): s drops out of the codes.
-    // A scale of 0 gives codes 0, a NaN one NaN.
+    // A scale of 0 gives codes 0, a NaN one NaN; below 1e-30 the quotient would pass fp32, so both move up.
     if (row_scale && lane == 0 && (kWarpRow || warp == 0)) a.scales[r] = s * top * (1.f / 448.f);
     auto factor = [&](float m) {
-      const float scaled = s * m;
-      return scaled == 0.f ? 0.f : scaled != scaled ? scaled : 448.f / m;
+      const float scaled = s * m, up = m < 1e-30f ? 0x1p90f : 1.f;
+      return scaled == 0.f ? make_float2(0.f, 0.f) : scaled != scaled ? make_float2(scaled, scaled) : make_float2(up, 448.f / (m * up));
     };
     uint8_t *o = static_cast<uint8_t *>(a.out) + r * a.out_stride;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c0 = first_column(v);
       if (c0 >= a.dim) break;
-      float q[8];
       if (kVec || row_scale) {
         float m = top;
         if (!row_scale) {  // group / 8 neighbouring lanes
-          m = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(h[v][e]));
-          m = warp_max(m, a.group / 8);
+          m = warp_max(max8(0.f, h[v]), a.group / 8);
           const int c = c0 + 8 * lane;
-          if (c < a.dim && (lane & (a.group / 8 - 1)) == 0) a.scales[r * groups + c / a.group] = s * m * (1.f / 448.f);
+          if (c < a.dim && (lane & (a.group / 8 - 1)) == 0) a.scales[r * groups + (c >> plan.log2_group)] = s * m * (1.f / 448.f);
         }
-        if (m < 1e-30f) {  // 448 / m would pass fp32
-          m *= 0x1p90f;
+        const float2 f = factor(m);
+        if (f.x > 1.f)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[v][e] *= 0x1p90f;
-        }
-        const float f = factor(m);
+          for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(f.x, f.x));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = h[v][e] * f;
+        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(f.y, f.y));
       } else {  // group / 32 values of every lane
         const int n = a.group / 32;
         float gm[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float m = warp_max(fabsf(h[v][e]), 32);
+          const float m = warp_max(fabsf(e & 1 ? h[v][e / 2].y : h[v][e / 2].x), 32);
           gm[e] = e % n ? max_nan(gm[e ? e - 1 : 0], m) : m;
         }
 #pragma unroll
@@ -214,26 +263,198 @@ __global__ void __launch_bounds__(32 * kMaxWarps, V <= 2 ? 2 : 1) rms_norm_kerne
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (lane == 0 && e % n == 0 && c0 + 32 * e < a.dim)
-            a.scales[r * groups + (c0 + 32 * e) / a.group] = s * gm[e] * (1.f / 448.f);
-          const float up = gm[e] < 1e-30f ? 0x1p90f : 1.f;
-          q[e] = h[v][e] * up * factor(gm[e] * up);
+            a.scales[r * groups + ((c0 + 32 * e) >> plan.log2_group)] = s * gm[e] * (1.f / 448.f);
+          const float2 f = factor(gm[e]);
+          float &q = e & 1 ? h[v][e / 2].y : h[v][e / 2].x;
+          q = q * f.x * f.y;
         }
       }
+      unsigned short b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __nv_cvt_float2_to_fp8x2(h[v][i], __NV_SATFINITE, __NV_E4M3);
       if constexpr (kVec) {
         const int c = c0 + 8 * lane;
-        if (c < a.dim) {
-          unsigned short b[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * e], q[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-          *reinterpret_cast<uint2 *>(o + c) = make_uint2(b[0] | (unsigned)b[1] << 16, b[2] | (unsigned)b[3] << 16);
-        }
+        if (c < a.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(b[0] | (unsigned)b[1] << 16, b[2] | (unsigned)b[3] << 16);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (column<false>(c0, lane, e) < a.dim) o[column<false>(c0, lane, e)] = __nv_cvt_float_to_fp8(q[e], __NV_SATFINITE, __NV_E4M3);
+          if (column<false>(c0, lane, e) < a.dim) o[column<false>(c0, lane, e)] = (uint8_t)(b[e / 2] >> (8 * (e & 1)));
       }
     }
   }
+}
+
+// Many rows of 513 to 8192 columns in 16-byte pieces: a block a row, two vectors a thread.  The loads of
+// kAhead rows are in flight at any time (asynchronous copies into shared memory, 48 KB a block at
+// 4096 columns of 16 bits), the weight stays in registers, and addresses advance by additions.
+// kMode: 0 the output is T, 1 e4m3 with a scale a row, 2 with a scale a group.
+constexpr int kAhead = 3;
+
+template <class T, int kMode, bool kRes>
+__global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_norm_args a, const Plan plan) {
+  constexpr int P = (int)sizeof(T) / 2;                  // 16-byte pieces of a vector
+  constexpr int kPieces = 2 * P * (kRes ? 2 : 1);        // of a thread's share of a row
+  extern __shared__ uint4 ring[];
+  __shared__ float red[2][2][16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int c0 = 256 * warp + 8 * lane, c1 = c0 + 256 * warps;
+  const bool in0 = c0 < a.dim, in1 = c1 < a.dim;
+  const long long first = blockIdx.x, step = gridDim.x;
+  const T *x = static_cast<const T *>(a.x) + first * a.x_stride + c0;
+  const T *res = kRes ? static_cast<const T *>(a.residual) + first * a.residual_stride + c0 : nullptr;
+  T *res_out = kRes && a.residual_out ? static_cast<T *>(a.residual_out) + first * a.residual_out_stride + c0 : nullptr;
+  const int out_size = kMode == 0 ? (int)sizeof(T) : 1;
+  char *out = static_cast<char *>(a.out) + (first * a.out_stride + c0) * out_size;
+  const int far = c1 - c0;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, pstep = blockDim.x * 16;
+
+  int todo = (int)((a.rows - first + step - 1) / step), ahead = todo;  // rows to work on, rows to load
+  auto copy_row = [&](uint32_t at) {
+    if (ahead > 0) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (in0) copy_async(at + i * pstep, reinterpret_cast<const uint4 *>(x) + i);
+        if (in1) copy_async(at + (P + i) * pstep, reinterpret_cast<const uint4 *>(x + far) + i);
+        if constexpr (kRes) {
+          if (in0) copy_async(at + (2 * P + i) * pstep, reinterpret_cast<const uint4 *>(res) + i);
+          if (in1) copy_async(at + (3 * P + i) * pstep, reinterpret_cast<const uint4 *>(res + far) + i);
+        }
+      }
+      --ahead;
+      x += step * a.x_stride;
+      if constexpr (kRes) res += step * a.residual_stride;
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) copy_row(mine + i * kPieces * pstep);
+  // zeros past the row's end, once
+  for (int i = 0; i < kAhead * kPieces; ++i)
+    if (!(i / P % 2 ? in1 : in0)) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(mine + i * pstep), "r"(0));
+  float2 w[2][4];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[v][i] = make_float2(1.f, 1.f);
+    times_weight<true>(a, plan.wide, 256 * (v * warps + warp), lane, w[v]);
+  }
+  const int groups = kMode == 2 ? (a.dim + a.group - 1) / a.group : 1;
+  float *scales = kMode == 0 ? nullptr : a.scales + first * groups;
+  uint32_t at = mine;
+  const uint32_t end = mine + kAhead * kPieces * pstep;
+  for (int buf = 0; todo > 0; --todo, buf ^= 1) {
+    copy_wait<kAhead - 1>();
+    float2 h[2][4], s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      Raw<T, true> xr, rr;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        xr.v[i] = load_shared(at + (v * P + i) * pstep);
+        if constexpr (kRes) rr.v[i] = load_shared(at + ((2 + v) * P + i) * pstep);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[v][i] = kRes ? __fadd2_rn(xr.pair(i), rr.pair(i)) : xr.pair(i);
+        s2 = __ffma2_rn(h[v][i], h[v][i], s2);
+      }
+    }
+    if constexpr (kRes)
+      if (res_out) {
+        if (in0) store8<T, true>(res_out, 0, 0, 1, h[0]);
+        if (in1) store8<T, true>(res_out + far, 0, 0, 1, h[1]);
+        res_out += step * a.residual_out_stride;
+      }
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], w[v][i]);
+    float ss = s2.x + s2.y, top = 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if constexpr (kMode == 1) {
+      top = max8(max8(0.f, h[0]), h[1]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (lane == 0) {
+      red[buf][0][warp] = ss;
+      if constexpr (kMode == 1) red[buf][1][warp] = top;
+    }
+    __syncthreads();  // (the other buffer is read before the next one's barrier)
+    copy_row(at);     // into the place just read
+    at += kPieces * pstep;
+    if (at == end) at = mine;
+    ss = (lane & 15) < warps ? red[buf][0][lane & 15] : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if constexpr (kMode == 1) {
+      top = (lane & 15) < warps ? red[buf][1][lane & 15] : 0.f;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    const float mean = ss * plan.inv_dim;
+    float s = rsqrtf(a.clamp ? mean : mean + a.eps);
+    if (a.clamp && s > plan.inv_eps) s = plan.inv_eps;
+    if constexpr (kMode == 0) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(s, s));
+      T *o = reinterpret_cast<T *>(out);
+      if (in0) store8<T, true>(o, 0, 0, 1, h[0]);
+      if (in1) store8<T, true>(o + far, 0, 0, 1, h[1]);
+    } else {
+      if (kMode == 1 && threadIdx.x == 0) scales[0] = s * top * (1.f / 448.f);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float m = top;
+        const bool in = v ? in1 : in0;
+        if constexpr (kMode == 2) {  // group / 8 neighbouring lanes
+          m = max8(0.f, h[v]);
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (plan.log2_group > 5) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          if (plan.log2_group > 6) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          const int c = v ? c1 : c0;
+          if (in && (c & (a.group - 1)) == 0) scales[c >> plan.log2_group] = s * m * (1.f / 448.f);
+        }
+        const float scaled = s * m;
+        float f = __fdividef(448.f, m);  // (within 2 units in the last place)
+        if (!(scaled > 0.f && m > 1e-30f && m < 1e30f)) {
+          // a scale of 0 gives codes 0, a NaN one NaN; where the quotient would leave fp32's range h w moves first
+          if (scaled == 0.f || scaled != scaled) {
+            f = scaled;
+          } else {
+            const float up = m < 1.f ? 0x1p90f : 0x1p-30f;
+            f = 448.f / (m * up);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(up, up));
+          }
+        }
+        unsigned short b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          b[i] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(h[v][i], make_float2(f, f)), __NV_SATFINITE, __NV_E4M3);
+        if (in) *reinterpret_cast<uint2 *>(out + (v ? far : 0)) = make_uint2(b[0] | (unsigned)b[1] << 16, b[2] | (unsigned)b[3] << 16);
+      }
+      scales += step * groups;
+    }
+    out += step * a.out_stride * out_size;
+  }
+  copy_wait<0>();
+}
+
+template <class T, int kMode, bool kRes>
+cudaError_t launch_stream(const mrf_rms_norm_args &a, const Plan &p, cudaStream_t st) {
+  auto *k = rms_norm_stream_kernel<T, kMode, kRes>;
+  const int warps = ((a.dim + 255) / 256 + 1) / 2;
+  const int smem = kAhead * (kRes ? 2 : 1) * 2 * (int)sizeof(T) / 2 * 16 * 32 * warps;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int blocks = std::max(1, std::min(32 / warps, 220 * 1024 / (smem + 1280)));  // on an SM, at 64 registers a thread
+  k<<<(int)std::min<long long>(a.rows, 148 * blocks), 32 * warps, smem, st>>>(a, p);
+  return cudaGetLastError();
 }
 
 bool vec_ok(const void *p, long long rows, long long stride, int size) {
@@ -243,20 +464,39 @@ bool vec_ok(const void *p, long long rows, long long stride, int size) {
 }
 
 template <class T, bool kVec>
-void launch(const mrf_rms_norm_args &a, cudaStream_t st) {
-  const bool wide = a.weight_dtype == MRF_DTYPE_F32 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+cudaError_t launch(const mrf_rms_norm_args &a, cudaStream_t st) {
+  Plan p;
+  p.wide = a.weight_dtype == MRF_DTYPE_F32 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+  p.inv_dim = 1.f / (float)a.dim;
+  p.inv_eps = 1.f / a.eps;
+  p.log2_group = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   const int chunks = (a.dim + 255) / 256;  // of 256 columns: a vector of each lane of a warp
+  const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs: more threads a row, shorter chains
   if (chunks <= 2) {
-    const int warps = a.rows >= 148 * 16 ? 8 : 1;  // few rows: an SM each
-    const int grid = (int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 32 / warps);
-    if (chunks == 1) rms_norm_kernel<T, 1, true, kVec><<<grid, 32 * warps, 0, st>>>(a, wide);
-    else rms_norm_kernel<T, 2, true, kVec><<<grid, 32 * warps, 0, st>>>(a, wide);
-    return;
+    const int warps = few ? 1 : 8;
+    const int grid = (int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 64 / warps);
+    if (chunks == 1) rms_norm_kernel<T, 1, true, kVec><<<grid, 32 * warps, 0, st>>>(a, p);
+    else rms_norm_kernel<T, 2, true, kVec><<<grid, 32 * warps, 0, st>>>(a, p);
+    return cudaGetLastError();
   }
-  const int vecs = chunks <= 2 * kMaxWarps ? 2 : 4, warps = (chunks + vecs - 1) / vecs;
-  const int grid = (int)std::min<long long>(a.rows, 148 * std::max(1, (vecs == 2 ? 32 : 16) / warps));
-  if (vecs == 2) rms_norm_kernel<T, 2, false, kVec><<<grid, 32 * warps, 0, st>>>(a, wide);
-  else rms_norm_kernel<T, 4, false, kVec><<<grid, 32 * warps, 0, st>>>(a, wide);
+  if (few && chunks <= 16) {
+    rms_norm_kernel<T, 1, false, kVec><<<(int)a.rows, 32 * chunks, 0, st>>>(a, p);
+    return cudaGetLastError();
+  }
+  if (chunks <= 32) {
+    if constexpr (kVec) {
+      if (!few) {
+        const int mode = a.out_dtype != MRF_DTYPE_E4M3 ? 0 : a.group == 0 ? 1 : 2;
+        if (a.residual) return mode == 0 ? launch_stream<T, 0, true>(a, p, st) : mode == 1 ? launch_stream<T, 1, true>(a, p, st) : launch_stream<T, 2, true>(a, p, st);
+        return mode == 0 ? launch_stream<T, 0, false>(a, p, st) : mode == 1 ? launch_stream<T, 1, false>(a, p, st) : launch_stream<T, 2, false>(a, p, st);
+      }
+    }
+    const int warps = (chunks + 1) / 2;
+    rms_norm_kernel<T, 2, false, kVec><<<(int)std::min<long long>(a.rows, 148 * (32 / warps)), 32 * warps, 0, st>>>(a, p);
+    return cudaGetLastError();
+  }
+  rms_norm_kernel<T, 5, false, kVec><<<(int)std::min<long long>(a.rows, 148), 32 * ((chunks + 4) / 5), 0, st>>>(a, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -267,12 +507,9 @@ cudaError_t launch_rms_norm(const mrf_rms_norm_args &a, cudaStream_t st) {
                    (!a.residual || vec_ok(a.residual, a.rows, a.residual_stride, size)) &&
                    (!a.residual_out || vec_ok(a.residual_out, a.rows, a.residual_out_stride, size)) &&
                    vec_ok(a.out, a.rows, a.out_stride, a.out_dtype == MRF_DTYPE_E4M3 ? 1 : size);
-#define MRF_NORM(T) (vec ? launch<T, true>(a, st) : launch<T, false>(a, st))
-  if (a.dtype == MRF_DTYPE_F32) MRF_NORM(float);
-  else if (a.dtype == MRF_DTYPE_F16) MRF_NORM(__half);
-  else MRF_NORM(__nv_bfloat16);
-#undef MRF_NORM
-  return cudaGetLastError();
+  if (a.dtype == MRF_DTYPE_F32) return vec ? launch<float, true>(a, st) : launch<float, false>(a, st);
+  if (a.dtype == MRF_DTYPE_F16) return vec ? launch<__half, true>(a, st) : launch<__half, false>(a, st);
+  return vec ? launch<__nv_bfloat16, true>(a, st) : launch<__nv_bfloat16, false>(a, st);
 }
 
 }  // namespace mrf

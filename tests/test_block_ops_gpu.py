@@ -31,7 +31,7 @@ def within(got, ref, bound, what=""):
 # ------------------------------------------------------------------------------------------ norm
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("rows,dim", [(1, 1), (3, 7), (5, 64), (1, 384), (301, 384), (2, 1000), (33, 1536), (7, 2049), (130, 4096),
-                                      (3, 8200), (2, 16384)])
+                                      (3, 8200), (2, 16384), (700, 1000), (601, 4104), (1500, 520), (593, 8192), (640, 1003)])
 def test_norm(dtype, rows, dim):
     g = gen(rows * dim)
     x, res = randn(g, rows, dim, dtype=dtype), 3 * randn(g, rows, dim)
@@ -63,7 +63,8 @@ def check_quant(r, y, group, dim):
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("rows,dim,group", [(1, 4096, 0), (9, 384, 128), (5, 1000, 64), (3, 77, 32), (2, 130, 128), (65, 2048, 32),
-                                            (4, 8192, 128), (2, 16384, 0), (17, 64, 0)])
+                                            (4, 8192, 128), (2, 16384, 0), (17, 64, 0), (650, 1000, 64), (600, 2048, 0), (1201, 640, 32),
+                                            (600, 8192, 128), (700, 1003, 128), (2500, 192, 64)])
 def test_norm_e4m3(dtype, rows, dim, group):
     g = gen(dim + group)
     x, res = randn(g, rows, dim, dtype=dtype), randn(g, rows, dim, dtype=dtype)
@@ -84,6 +85,13 @@ def test_norm_zero_nan_and_infinity():
     assert r.scales[1].isnan().all() and r.out[1].float().isnan().all()
     assert r.scales[2, 0].isnan() and r.out[2, :64].float().isnan().all()
     assert torch.equal(r.out[3].float(), torch.full((256,), 448.0, device="cuda"))
+    many = torch.cat((x.repeat(1, 3), torch.full((4, 768), 2.0**-100, device="cuda", dtype=BF16)) * 100)  # rows enough for the streaming kernel
+    q = mrf.rms_norm(many, None, 1e-6, out_dtype=E4M3, group=64)
+    assert not q.out[0].float().any() and not q.scales[0].any() and q.out[1].float().isnan().all() and q.scales[2, 0].isnan()
+    assert not q.out[2, 64:256].float().any() and torch.equal(q.out[3].float(), torch.full((768,), 448.0, device="cuda"))
+    # 2^-100 / sqrt(1e-6): a scale of 1000 * 2^-100 / 448 and full codes
+    assert torch.equal(q.out[4].float(), torch.full((768,), 448.0, device="cuda"))
+    within(q.scales[4], torch.full((12,), 1000 * 2.0**-100 / 448, device="cuda", dtype=torch.float64), torch.tensor(1000 * 2.0**-100 / 448 * 2.0**-18, device="cuda"))
     y = mrf.rms_norm(x, None, 1e-6).out
     assert torch.equal(y[0].float(), torch.zeros(256, device="cuda")) and y[1].isnan().all() and y[2, 7].isnan()
 
