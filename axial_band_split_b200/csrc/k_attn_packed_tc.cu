@@ -6,7 +6,7 @@
 // Tiles.  The G = heads / kv_heads query heads that share a key head are rows of one matrix: a tile
 // is TQ = 128 / G tokens x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
 // box per 64 dimensions), so each key block is read once for all of them and a single new token
-// already fills G rows.  Key blocks are 128 rows.
+// already fills G rows.  Key blocks are 64 rows.
 //
 // Work items.  A CTA runs two units (a tile with a range of keys) t = 0, 1 side by side:
 //   pair   - two neighbouring tiles of one sequence and key head: they share every key block;
@@ -20,9 +20,19 @@
 // through a ring in shared memory.
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, one score row per thread; warp 8: bulk tensor loads;
-// warps 9, 10: matrix instructions of unit 0, 1; warp 11: items.  Tensor memory (512 columns): with
-// v up to 64 wide S_t at 128 t, O_t at 256 + 64 t, P_t at 384 + 64 t; with wider v S_t at 128 t and
-// O_t at 256 + 128 t, and P_t (16-bit, half as wide) overwrites S_t once the softmax has read it.
+// warps 9, 10: matrix instructions of unit 0, 1; warp 11: items.
+//
+// Places.  The scores of a unit's key blocks take turns in two places of 64 columns in tensor memory
+// (S_t at 128 t; O_t at 256), and the 16-bit probabilities P overwrite the scores they came from: the
+// softmax reads block i into registers, writes P(i), the issuer queues P(i) V and behind it, in the
+// tensor core's own order, the scores of block i + 2 into the same place.  So while the matrix
+// instructions of one block run, the softmax works on the other, and with both units the exponentials
+// rarely wait for a chain of products.
+//
+// K and V blocks stream through one ring in the order of their use, K0 K1 V0 K2 V1 ... (separate keys:
+// the two units' streams take turns).  Both issuers acknowledge every slot, their own when its reads have ended and
+// the other unit's as it arrives: a phase of a slot's barrier is then never more than one ahead of
+// anybody who waits on it by parity.
 //
 // Key rows past a sequence's end belong to others or were never written: their scores are replaced
 // by -inf whatever they are, and their rows of v, whose product with a zero probability could still
@@ -38,7 +48,8 @@
 namespace mrf {
 namespace {
 
-constexpr int kRows = 128, kKeys = 128, kAtom = 16384;  // one atom: 128 rows x 64 16-bit values
+constexpr int kRows = 128, kKeys = 64;
+constexpr int kAtom = kRows * 128, kKAtom = kKeys * 128;  // 64 16-bit values of a tile's or a key block's rows
 constexpr int kThreads = 384;
 // register split, as in the model's attention: 2 * 128 * 208 + 128 * 72 <= 384 * 168
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
@@ -63,10 +74,9 @@ struct Item {
 
 template <int QA, int VA>
 struct Cfg {
-  static constexpr bool overlay = VA == 2;           // P over S in tensor memory
   static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
-  static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
-  static constexpr int slots = 10 * kAtom / slot;    // ring of K or V blocks
+  static constexpr int slot = (QA > VA ? QA : VA) * kKAtom;
+  static constexpr int slots = slot > kKAtom ? 10 : 16;  // ring of K or V blocks
   static constexpr int q = 0;
   static constexpr int kv = 4 * kAtom;
   static constexpr int bar = kv + slots * slot;
@@ -138,19 +148,44 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (+)= A * B with A (16-bit pairs) in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc ? 1u : 0u));
+// Matrix instructions of a whole warp, issued by its `leader` lane alone: without a branch around them
+// the operands stay in uniform registers (inside one, each cost about 130 clk to issue).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p;
 }
+// D (+)= A * B, both from shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc), "r"(leader));
+}
+// D (+)= A * B with A (16-bit pairs) in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// V as the MN-major B operand: 64-wide atoms of 16 KB side by side (the leading offset), 8 keys each
-// 1024 bytes (the stride offset).
+// V as the MN-major B operand: 64-wide atoms side by side (the leading offset), 8 keys each 1024 bytes
+// (the stride offset).
 __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kAtom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kKAtom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
@@ -225,10 +260,10 @@ __device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
   return it;
 }
 
-// Order of an item's ring slots.  Each unit's key stream is K0 K1 V0 K2 V1 ... V(n-1): element i of it.
+// A stream of n key blocks in the order of its use: K0 K1 V0 K2 V1 ... V(n - 1).  The elements of block j.
 __device__ __forceinline__ int k_elem(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_elem(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
-// Separate keys: the two streams take turns while both last.
+// Place in an item's ring order of element e of unit t.
 __device__ __forceinline__ int slot_of(const Item &it, int t, int e) {
   if (it.shared) return e;
   return t == 0 ? e + min(e, 2 * it.u[1].nblk) : e + min(e + 1, 2 * it.u[0].nblk);
@@ -239,14 +274,14 @@ __device__ __forceinline__ int item_slots(const Item &it) {
 
 // ------------------------------------------------------------------ softmax of one key block
 __device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
-  float ma = s[0], mb = s[32], mc = s[64], md = s[96];
+  float ma = s[0], mb = s[16], mc = s[32], md = s[48];
 #pragma unroll
-  for (int i = 1; i < 32; i += 2) {
-    const int i2 = i + 1 < 32 ? i + 1 : i;
+  for (int i = 1; i < 16; i += 2) {
+    const int i2 = i + 1 < 16 ? i + 1 : i;
     ma = max3(ma, s[i], s[i2]);
-    mb = max3(mb, s[32 + i], s[32 + i2]);
-    mc = max3(mc, s[64 + i], s[64 + i2]);
-    md = max3(md, s[96 + i], s[96 + i2]);
+    mb = max3(mb, s[16 + i], s[16 + i2]);
+    mc = max3(mc, s[32 + i], s[32 + i2]);
+    md = max3(md, s[48 + i], s[48 + i2]);
   }
   return fmaxf(fmaxf(ma, mb), fmaxf(mc, md));
 }
@@ -261,13 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bar);
   uint64_t *q_full = bars, *q_empty = bars + 2;          // [qbufs]
-  uint64_t *s_full = bars + 4, *s_free = bars + 6;       // [2]: scores written / read
-  uint64_t *p_full = bars + 8, *pv_done = bars + 10;     // [2]
-  uint64_t *o_free = bars + 12;                          // [2]
-  uint64_t *item_full = bars + 14, *item_empty = bars + 18;  // [kItems]
-  uint64_t *done = bars + 22;
-  uint64_t *kv_full = bars + 23, *kv_empty = kv_full + C::slots;
-  static_assert(23 + 2 * C::slots <= 62, "barrier area");
+  uint64_t *s_full = bars + 4, *p_full = bars + 8;       // [2 t + place]
+  uint64_t *pv_done = bars + 12, *o_free = bars + 14;    // [2]
+  uint64_t *item_full = bars + 16, *item_empty = bars + 20;  // [kItems]
+  uint64_t *done = bars + 24;
+  uint64_t *kv_full = bars + 25, *kv_empty = kv_full + C::slots;
+  static_assert(25 + 2 * C::slots <= 62, "barrier area");
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 62);
   volatile int *abort = reinterpret_cast<int *>(bars + 63);
   Item *items = reinterpret_cast<Item *>(smem + C::item);
@@ -278,13 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     for (int b = 0; b < C::qbufs; ++b) { tc::mbar_init(q_full + b, 1); tc::mbar_init(q_empty + b, 2); }
     for (int s = 0; s < C::slots; ++s) { tc::mbar_init(kv_full + s, 1); tc::mbar_init(kv_empty + s, 2); }
-    for (int t = 0; t < 2; ++t) {
-      tc::mbar_init(s_full + t, 1);
-      tc::mbar_init(s_free + t, 4);
-      tc::mbar_init(p_full + t, 4);
-      tc::mbar_init(pv_done + t, 1);
-      tc::mbar_init(o_free + t, 4);
-    }
+    for (int i = 0; i < 4; ++i) { tc::mbar_init(s_full + i, 1); tc::mbar_init(p_full + i, 4); }
+    for (int t = 0; t < 2; ++t) { tc::mbar_init(pv_done + t, 1); tc::mbar_init(o_free + t, 4); }
     for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 11); }
     tc::mbar_init(done, 2);
     tc::fence_barrier_init();
@@ -381,22 +410,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = g % C::slots;
             if (!tc::mbar_wait(kv_empty + s, ((g / C::slots) & 1) ^ 1, status, 53, abort)) return false;
             const bool is_k = e == 0 || ((e & 1) && e != 2 * nb - 1);
-            const int j = is_k ? (e + 1) / 2 : e == 2 * nb - 1 ? nb - 1 : e / 2 - 1;
-            tc::mbar_arrive_expect_tx(kv_full + s, (is_k ? QA : VA) * kAtom);
-            for (int c = 0; c < (is_k ? QA : VA); ++c)
-              tc::tma_load_3d(smem + C::kv + s * C::slot + c * kAtom, is_k ? &tk : &tv, kv_full + s, 64 * c, it.u[t].kvh,
+            const int j = is_k ? (e + 1) / 2 : e == 2 * nb - 1 ? nb - 1 : e / 2 - 1, atoms = is_k ? QA : VA;
+            tc::mbar_arrive_expect_tx(kv_full + s, atoms * kKAtom);
+            for (int c = 0; c < atoms; ++c)
+              tc::tma_load_3d(smem + C::kv + s * C::slot + c * kKAtom, is_k ? &tk : &tv, kv_full + s, 64 * c, it.u[t].kvh,
                               it.u[t].k_row + j * kKeys);
             ++g;
             return true;
           };
-          if (it.shared) {
-            const int nb = max(n0, n1);
-            for (int e = 0; ok && e < 2 * nb; ++e) ok = fill(0, e, nb);
-          } else {
-            for (int e = 0; ok && e < 2 * max(n0, n1); ++e) {
-              if (e < 2 * n0) ok = fill(0, e, n0);
-              if (ok && e < 2 * n1) ok = fill(1, e, n1);
-            }
+          const int nmax = max(n0, n1);
+          for (int e = 0; ok && e < 2 * nmax; ++e) {
+            if (it.shared || e < 2 * n0) ok = fill(0, e, it.shared ? nmax : n0);
+            if (ok && !it.shared && e < 2 * n1) ok = fill(1, e, n1);
           }
           ++qn;
         }
@@ -408,99 +433,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------- matrix instructions of unit t
-      const int t = warp - 9;
+      const int t = uniform(warp - 9);
+      const uint32_t leader = elect_lane();
       Item it;
       const uint32_t id_s = tc::idesc_f16(kRows, kKeys, false, kBF);
       const uint32_t id_pv = tc::idesc_f16(kRows, (a.v_width + 15) / 16 * 16, true, kBF);
       const int qk_steps = (a.width + 15) / 16;
       const uint32_t tS = tmem + 128 * t, tO = tmem + kOCol + kOStep * t;
-      const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
-      int g0 = 0, qn = 0, blk = 0, units = 0;  // ring slots before this item, q buffers, blocks and units of this warp
+      int g0 = 0, qn = 0, units = 0;    // ring slots before this item, q buffers, units of this warp
+      uint32_t uses[2] = {0, 0};        // of each place
+      // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
+      // / 16, below 2^14 within shared memory)
+      const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * QA * kAtom);
+      const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::kv)), v_desc0 = v_desc(tc::smem_u32(smem + C::kv));
       bool ok = true;
       for (int n = 0; ok && next_item(n, it); ++n) {
-        const int nb = it.u[t].nblk, klen = it.u[t].klen;
-        const int all = it.shared ? max(it.u[0].nblk, it.u[1].nblk) : nb;  // blocks of the stream
-        const int used = item_slots(it);
+        const int nb = uniform(it.u[t].nblk), klen = uniform(it.u[t].klen);
+        const int all = uniform(it.shared ? max(it.u[0].nblk, it.u[1].nblk) : nb);  // blocks of the stream
+        const int used = uniform(item_slots(it));
         if (used == 0) continue;
         const int qb = qn % C::qbufs;
         // the keys that any token of the tile sees
-        const int seen = min(klen, it.u[t].lim0 + it.u[t].ntok - 1);
-        auto slot = [&](int e) { return g0 + slot_of(it, t, e); };
+        const int seen = uniform(nb > 0 ? min(klen, it.u[t].lim0 + it.u[t].ntok - 1) : 0);
+        int at = 0;  // ring order: slots of this item acknowledged or taken
         auto full = [&](int gs) { return tc::mbar_wait(kv_full + gs % C::slots, (gs / C::slots) & 1, status, 54, abort); };
-        auto release = [&](int gs) {  // the slot's reads are those of the instructions issued so far
-          tc::mma_commit(kv_empty + gs % C::slots);
-          if (!it.shared) tc::mma_commit(kv_empty + gs % C::slots);
-        };
-        auto issue_s = [&](int j) {
-          const int gs = slot(k_elem(j));
-          if (!full(gs)) return false;
-          tc::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t qa = tc::smem_u32(smem + C::q + (qb * 2 + t) * QA * kAtom);
-            const uint32_t ka = tc::smem_u32(smem + C::kv + (gs % C::slots) * C::slot);
-            for (int kk = 0; kk < qk_steps; ++kk)
-              tc::mma_f16(tS, tc::sw128_kmajor_desc(qa + (kk / 4) * kAtom + (kk % 4) * 32),
-                          tc::sw128_kmajor_desc(ka + (kk / 4) * kAtom + (kk % 4) * 32), id_s, kk != 0);
-            tc::mma_commit(s_full + t);
-            release(gs);
-            if (j == nb - 1) tc::mma_commit(q_empty + qb);
+        // acknowledges the slots before place `to`, which this unit does not read, as they arrive
+        auto pass = [&](int to) {
+          for (; at < to; ++at) {
+            if (!full(g0 + at)) return false;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(kv_empty + (g0 + at) % C::slots);
           }
-          __syncwarp();
+          return true;
+        };
+        // waits for element e of the own stream: its ring slot, or -1
+        auto take = [&](int e) {
+          const int place = uniform(slot_of(it, t, e));
+          if (!pass(place) || !full(g0 + place)) return -1;
+          at = place + 1;
+          return (g0 + place) % C::slots;
+        };
+        // scores of block i, into the place that P(i - 2) V, queued before, reads
+        auto issue_s = [&](int i) {
+          const int h = i & 1, sl = take(k_elem(i));
+          if (sl < 0) return false;
+          tc::tc_fence_after();
+          const uint64_t qd = q_desc + ((qb * 2 * QA * kAtom) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4 * QA; ++kk)
+            if (kk < qk_steps)
+              mma_ss(leader, tS + kKeys * h, qd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
+                     kd + (((kk / 4) * kKAtom + (kk % 4) * 32) >> 4), id_s, kk != 0);
+          commit(leader, s_full + 2 * t + h);
+          commit(leader, kv_empty + sl);
+          if (i == nb - 1) commit(leader, q_empty + qb);
           return true;
         };
         if (!tc::mbar_wait(q_full + qb, (qn / C::qbufs) & 1, status, 55, abort)) { ok = false; break; }
         if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qb);
-        for (int j = 0; j < nb; ++j, ++blk) {
-          if (C::overlay || j == 0) {
-            // S_t is free once the softmax has read it; with P_t on top, once P_t * V has ended
-            if (blk > 0 && !tc::mbar_wait((C::overlay ? pv_done : s_free) + t, (blk - 1) & 1, status, 56, abort)) { ok = false; break; }
-            if (!issue_s(j)) { ok = false; break; }
-          }
-          if (!C::overlay && j + 1 < nb) {  // the next block's scores under this block's exponentials
-            if (!tc::mbar_wait(s_free + t, blk & 1, status, 57, abort) || !issue_s(j + 1)) { ok = false; break; }
-          }
-          const int gs = slot(v_elem(j, all));
-          if (!full(gs)) { ok = false; break; }
-          uint8_t *vs = smem + C::kv + (gs % C::slots) * C::slot;
-          const int live = min(kKeys, klen - j * kKeys);          // the sequence's rows of this block
-          const int steps = (min(kKeys, seen - j * kKeys) + 15) / 16;  // 16-key steps that some token sees
+        if ((nb > 0 && !issue_s(0)) || (nb > 1 && !issue_s(1))) { ok = false; break; }
+        for (int i = 0; i < nb; ++i) {
+          const int h = i & 1, sl = take(v_elem(i, all));
+          if (sl < 0) { ok = false; break; }
+          const int live = min(kKeys, klen - i * kKeys);               // the sequence's rows of this block
+          const int steps = (min(kKeys, seen - i * kKeys) + 15) / 16;  // 16-key steps that some token sees
           if (live < 16 * steps) {
             // rows of no sequence: zeros, whatever they hold (both units of a pair write the same zeros)
+            uint8_t *vs = smem + C::kv + sl * C::slot;
             const int rows = 16 * steps - live;
             for (int c = lane; c < rows * 8 * VA; c += 32)
-              *reinterpret_cast<uint4 *>(vs + (c / (rows * 8)) * kAtom + (live + (c / 8) % rows) * 128 + (c % 8) * 16) =
+              *reinterpret_cast<uint4 *>(vs + (c / (rows * 8)) * kKAtom + (live + (c / 8) % rows) * 128 + (c % 8) * 16) =
                   make_uint4(0, 0, 0, 0);
             tc::fence_proxy_async();
             __syncwarp();
           }
-          if (!tc::mbar_wait(p_full + t, blk & 1, status, 58, abort) ||
-              (j == 0 && !tc::mbar_wait(o_free + t, (units & 1) ^ 1, status, 59, abort))) {
+          if (!tc::mbar_wait(p_full + 2 * t + h, uses[h] & 1, status, 58, abort) ||
+              (i == 0 && !tc::mbar_wait(o_free + t, (units & 1) ^ 1, status, 59, abort))) {
             ok = false;
             break;
           }
+          ++uses[h];
           tc::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t va = tc::smem_u32(vs);
-            for (int kk = 0; kk < steps; ++kk)
-              mma_ts(tO, tP + 8 * kk, v_desc(va + kk * 2048), id_pv, j != 0 || kk != 0);
-            tc::mma_commit(pv_done + t);
-            release(gs);
-          }
-          __syncwarp();
+          const uint64_t vd = v_desc0 + ((sl * C::slot) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < steps) mma_ts(leader, tO, tS + kKeys * h + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, i != 0 || kk != 0);
+          commit(leader, pv_done + t);
+          commit(leader, kv_empty + sl);
+          if (i + 2 < nb && !issue_s(i + 2)) { ok = false; break; }
         }
-        // a pair's first tile leaves the blocks that only the second sees, as they arrive
-        for (int j = nb; ok && j < all; ++j) {
-          for (int e : {k_elem(j), v_elem(j, all)}) {
-            const int gs = slot(e);
-            if (!full(gs)) { ok = false; break; }
-            if (lane == 0) tc::mbar_arrive(kv_empty + gs % C::slots);
-          }
-        }
+        // what is left of the item is the other unit's
+        if (ok && !pass(used)) ok = false;
         g0 += used;
         ++qn;
         units += nb > 0;
       }
-      if (lane == 0) tc::mma_commit(done);
+      commit(leader, done);
       tc::mbar_wait(done, 0, status, 60, abort);
       if (*abort && lane == 0) drain(done, 0);
     }
@@ -511,104 +539,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = r / a.G, head = r - tok * a.G;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + kOCol + kOStep * t + lane_off;
-    const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t + lane_off;
     const float c = a.scale_log2;
-    int blk = 0;
+    uint32_t uses[2] = {0, 0}, steps = 0;  // of each place, and blocks in all
     Item it;
     for (int n = 0; next_item(n, it); ++n) {
       const int nb = it.u[t].nblk;
       const bool row = tok < it.u[t].ntok && r < a.TQ * a.G;
       const bool live = __any_sync(0xffffffffu, row);  // a warp without rows only keeps the barriers going
-      const int vis = row ? max(0, min(it.u[t].klen, it.u[t].lim0 + tok)) : 0;
+      // the keys this row sees (a row that is none needs no mask)
+      const int vis = row ? max(0, min(it.u[t].klen, it.u[t].lim0 + tok)) : 0x7fffffff;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < nb; ++j, ++blk) {
-        if (!tc::mbar_wait(s_full + t, blk & 1, status, 61, abort)) { ok = false; break; }
+      for (int i = 0; i < nb; ++i, ++steps) {
+        const int h = i & 1;
+        // (these scores also say that P(i - 2) V has ended: the tensor core works in order)
+        if (!tc::mbar_wait(s_full + 2 * t + h, uses[h] & 1, status, 61, abort)) { ok = false; break; }
+        ++uses[h];
         tc::tc_fence_after();
-        if (!live) {
-          // its arrival for this block must not count for the one before: that block's P * V has ended
-          if (!C::overlay && lane == 0) tc::mbar_arrive(s_free + t);
-          if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 62, abort)) { ok = false; break; }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(p_full + t);
-          continue;
-        }
-        float sv[kKeys];
-        {
-          uint32_t raw[kKeys];
+        if (live) {
+          float sv[kKeys];
+          {
+            uint32_t raw[kKeys];
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(tS + i, raw + i);
-          tmem_wait_ld();
+            for (int k = 0; k < kKeys; k += 32) tmem_ld32_async(tS + kKeys * h + k, raw + k);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 32) tmem_landed(raw + i);
+            for (int k = 0; k < kKeys; k += 32) tmem_landed(raw + k);
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) sv[i] = __uint_as_float(raw[i]);
-        }
-        tc::tc_fence_before();
-        if (!C::overlay) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(s_free + t);
-        }
-        const int hi = vis - j * kKeys;
-        if (__any_sync(0xffffffffu, hi < kKeys)) {
+            for (int k = 0; k < kKeys; ++k) sv[k] = __uint_as_float(raw[k]);
+          }
+          const int hi = vis - i * kKeys;
+          if (__any_sync(0xffffffffu, hi < kKeys)) {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (i >= hi) sv[i] = -INFINITY;
-        }
-        const float bm = row_max(sv);
-        bool need = false;
-        float alpha = 1.f;
-        if (j == 0) {
-          m = bm;
-        } else {
-          need = (bm - m) * c > kRescaleLog2;  // also from -inf, whose l and O are zero
-          if (need) {
-            alpha = ex2((m - bm) * c);
-            l *= alpha;
+            for (int k = 0; k < kKeys; ++k)
+              if (k >= hi) sv[k] = -INFINITY;
+          }
+          const float bm = row_max(sv);
+          bool need = false;
+          float alpha = 1.f;
+          if (i == 0) {
             m = bm;
+          } else {
+            need = row && (bm - m) * c > kRescaleLog2;  // also from -inf, whose l and O are zero
+            if (need) {
+              alpha = ex2((m - bm) * c);
+              l *= alpha;
+              m = bm;
+            }
           }
-        }
-        // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
-        const float negm = m == -INFINITY ? 0.f : -m * c;
-        const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
-        uint32_t pk[kKeys / 2];
-        float2 sum[4] = {};
+          // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
+          const float negm = m == -INFINITY ? 0.f : -m * c;
+          const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
+          uint32_t pk[kKeys / 2];
+          float2 sum[4] = {};
 #pragma unroll
-        for (int i = 0; i < kKeys; i += 8) {
+          for (int k = 0; k < kKeys; k += 8) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 d = __ffma2_rn(make_float2(sv[i + 2 * u], sv[i + 2 * u + 1]), c2, n2);
-            const float2 p = make_float2(ex2(d.x), ex2(d.y));
-            sum[u] = __fadd2_rn(sum[u], p);
-            pk[(i >> 1) + u] = pack2<kBF>(p.x, p.y);
+            for (int u = 0; u < 4; ++u) {
+              const float2 d = __ffma2_rn(make_float2(sv[k + 2 * u], sv[k + 2 * u + 1]), c2, n2);
+              const float2 p = make_float2(ex2(d.x), ex2(d.y));
+              sum[u] = __fadd2_rn(sum[u], p);
+              pk[(k >> 1) + u] = pack2<kBF>(p.x, p.y);
+            }
           }
-        }
-        const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-        l += s4.x + s4.y;
-        // P_t and O_t are free once the previous block's P * V has ended (with P_t over S_t this
-        // block's scores were only issued then)
-        if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 62, abort)) { ok = false; break; }
-        tc::tc_fence_after();
+          const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l += s4.x + s4.y;
 #pragma unroll
-        for (int i = 0; i < kKeys / 2; i += 4) tmem_st4(tP + i, pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
-        tmem_wait_st();
-        if (__any_sync(0xffffffffu, need)) {
+          for (int k = 0; k < kKeys / 2; k += 4) tmem_st4(tS + kKeys * h + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
+          tmem_wait_st();
+          if (__any_sync(0xffffffffu, need)) {
+            // O_t moves to the new maximum once P(i - 1) V has ended
+            if (!tc::mbar_wait(pv_done + t, (steps - 1) & 1, status, 62, abort)) { ok = false; break; }
+            tc::tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 64 * VA; i += 32) {
-            float v[32];
-            tc::tmem_ld32(tO + i, v);
+            for (int k = 0; k < 64 * VA; k += 32) {
+              float v[32];
+              tc::tmem_ld32(tO + k, v);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= alpha;
-            tc::tmem_st32(tO + i, v);
+              for (int e = 0; e < 32; ++e) v[e] *= alpha;
+              tc::tmem_st32(tO + k, v);
+            }
           }
+          tc::tc_fence_before();
         }
-        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + t);
+        if (lane == 0) tc::mbar_arrive(p_full + 2 * t + h);
       }
       if (!ok) break;
       if (nb > 0) {
-        if (!tc::mbar_wait(pv_done + t, (blk - 1) & 1, status, 63, abort)) break;
+        // the last product; first the one before it, so that one phase at most is outstanding
+        if (nb > 1 && !tc::mbar_wait(pv_done + t, (steps - 2) & 1, status, 63, abort)) break;
+        if (!tc::mbar_wait(pv_done + t, (steps - 1) & 1, status, 63, abort)) break;
         tc::tc_fence_after();
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that saw no key: zeros

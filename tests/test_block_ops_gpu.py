@@ -294,6 +294,18 @@ def test_attention_long(causal):
     run(Shape([(1, 70001)], 2, 2, 64, 64, F16, causal))
 
 
+def test_attention_cold_inputs_give_the_same_bits():
+    """The first call on inputs that no cache holds yet (slow loads, units that run apart) against the calls after it."""
+    for i in range(6):
+        for s in (Shape([(1, 7000)] * 32, 32, 8, 128, 128, max_k=7000), Shape([(1, 30000), (2, 9000)], 8, 1, 128, 128, max_k=30000),
+                  Shape([(1, 5000)] * 40 + [(1, 10)] * 40, 6, 3, 64, 64, max_k=5000)):
+            q, k, v, offsets, start, length, spans = make(s, 100 + i)
+            torch.cuda.synchronize()
+            outs = [mrf.attention_packed(q, k, v, offsets, start, length, s.max_k) for _ in range(4)]
+            n = sum(p[1] for p in spans)
+            assert all(torch.equal(o[:n], outs[-1][:n]) for o in outs[:-1])
+
+
 def test_attention_large_scores_and_peaks():
     """Scores of hundreds (running maxima that jump between key blocks) and one key that takes all the weight."""
     for width in (64, 128):
