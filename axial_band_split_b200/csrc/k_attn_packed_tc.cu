@@ -261,16 +261,8 @@ __device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
 }
 
 // A stream of n key blocks in the order of its use: K0 K1 V0 K2 V1 ... V(n - 1).  The elements of block j.
-__device__ __forceinline__ int k_elem(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int v_elem(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
-// Place in an item's ring order of element e of unit t.
-__device__ __forceinline__ int slot_of(const Item &it, int t, int e) {
-  if (it.shared) return e;
-  return t == 0 ? e + min(e, 2 * it.u[1].nblk) : e + min(e + 1, 2 * it.u[0].nblk);
-}
-__device__ __forceinline__ int item_slots(const Item &it) {
-  return it.shared ? 2 * max(it.u[0].nblk, it.u[1].nblk) : 2 * (it.u[0].nblk + it.u[1].nblk);
-}
+__device__ __forceinline__ int k_elem(int j) { return max(0, 2 * j - 1); }
+__device__ __forceinline__ int v_elem(int j, int n) { return min(2 * j + 2, 2 * n - 1); }
 
 // ------------------------------------------------------------------ softmax of one key block
 __device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
@@ -440,45 +432,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_pv = tc::idesc_f16(kRows, (a.v_width + 15) / 16 * 16, true, kBF);
       const int qk_steps = (a.width + 15) / 16;
       const uint32_t tS = tmem + 128 * t, tO = tmem + kOCol + kOStep * t;
-      int g0 = 0, qn = 0, units = 0;    // ring slots before this item, q buffers, units of this warp
-      uint32_t uses[2] = {0, 0};        // of each place
+      int ring = 0, qn = 0;             // next ring slot, q buffer
+      uint32_t ring_phase = 0, q_phase = 0, units = 0, uses[2] = {0, 0};  // parities: of those, of units, of the places' uses
       // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
       // / 16, below 2^14 within shared memory)
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * QA * kAtom);
       const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::kv)), v_desc0 = v_desc(tc::smem_u32(smem + C::kv));
       bool ok = true;
       for (int n = 0; ok && next_item(n, it); ++n) {
-        const int nb = uniform(it.u[t].nblk), klen = uniform(it.u[t].klen);
-        const int all = uniform(it.shared ? max(it.u[0].nblk, it.u[1].nblk) : nb);  // blocks of the stream
-        const int used = uniform(item_slots(it));
+        const int n0 = uniform(it.u[0].nblk), n1 = uniform(it.u[1].nblk), shared = uniform(it.shared);
+        const int nb = t ? n1 : n0;
+        const int all = shared ? max(n0, n1) : nb;                   // blocks of the stream
+        const int others = shared ? 0 : 2 * (t ? n0 : n1);           // ring slots of the other unit's
+        const int used = 2 * all + others;
         if (used == 0) continue;
-        const int qb = qn % C::qbufs;
+        const int klen = uniform(t ? it.u[1].klen : it.u[0].klen);
         // the keys that any token of the tile sees
-        const int seen = uniform(nb > 0 ? min(klen, it.u[t].lim0 + it.u[t].ntok - 1) : 0);
-        int at = 0;  // ring order: slots of this item acknowledged or taken
-        auto full = [&](int gs) { return tc::mbar_wait(kv_full + gs % C::slots, (gs / C::slots) & 1, status, 54, abort); };
+        const int seen = uniform(min(klen, t ? it.u[1].lim0 + it.u[1].ntok - 1 : it.u[0].lim0 + it.u[0].ntok - 1));
+        int at = 0;  // slots of this item acknowledged or taken
+        auto full = [&]() { return tc::mbar_wait(kv_full + ring, ring_phase, status, 54, abort); };
+        auto advance = [&]() {
+          ++at;
+          if (++ring == C::slots) {
+            ring = 0;
+            ring_phase ^= 1;
+          }
+        };
         // acknowledges the slots before place `to`, which this unit does not read, as they arrive
         auto pass = [&](int to) {
-          for (; at < to; ++at) {
-            if (!full(g0 + at)) return false;
+          while (at < to) {
+            if (!full()) return false;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(kv_empty + (g0 + at) % C::slots);
+            if (lane == 0) tc::mbar_arrive(kv_empty + ring);
+            advance();
           }
           return true;
         };
-        // waits for element e of the own stream: its ring slot, or -1
+        // waits for element e of the own stream (the two streams take turns while both last): its
+        // slot, or -1
         auto take = [&](int e) {
-          const int place = uniform(slot_of(it, t, e));
-          if (!pass(place) || !full(g0 + place)) return -1;
-          at = place + 1;
-          return (g0 + place) % C::slots;
+          if (!pass(e + min(e + t, others)) || !full()) return -1;
+          const int sl = ring;
+          advance();
+          return sl;
         };
         // scores of block i, into the place that P(i - 2) V, queued before, reads
-        auto issue_s = [&](int i) {
-          const int h = i & 1, sl = take(k_elem(i));
-          if (sl < 0) return false;
+        auto issue_s = [&](int i, int sl) {
+          const int h = i & 1;
           tc::tc_fence_after();
-          const uint64_t qd = q_desc + ((qb * 2 * QA * kAtom) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
+          const uint64_t qd = q_desc + ((qn * 2 * QA * kAtom) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4 * QA; ++kk)
             if (kk < qk_steps)
@@ -486,15 +488,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                      kd + (((kk / 4) * kKAtom + (kk % 4) * 32) >> 4), id_s, kk != 0);
           commit(leader, s_full + 2 * t + h);
           commit(leader, kv_empty + sl);
-          if (i == nb - 1) commit(leader, q_empty + qb);
-          return true;
+          if (i == nb - 1) commit(leader, q_empty + qn);
         };
-        if (!tc::mbar_wait(q_full + qb, (qn / C::qbufs) & 1, status, 55, abort)) { ok = false; break; }
-        if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qb);
-        if ((nb > 0 && !issue_s(0)) || (nb > 1 && !issue_s(1))) { ok = false; break; }
+        if (!tc::mbar_wait(q_full + qn, q_phase, status, 55, abort)) { ok = false; break; }
+        if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qn);
+        for (int i = 0; ok && i < min(nb, 2); ++i) {
+          const int sl = take(k_elem(i));
+          if (sl < 0) ok = false;
+          else issue_s(i, sl);
+        }
+        if (!ok) break;
         for (int i = 0; i < nb; ++i) {
           const int h = i & 1, sl = take(v_elem(i, all));
-          if (sl < 0) { ok = false; break; }
+          const int sk = i + 2 < nb && sl >= 0 ? take(k_elem(i + 2)) : 0;  // ahead of the wait for P(i)
+          if (sl < 0 || sk < 0) { ok = false; break; }
           const int live = min(kKeys, klen - i * kKeys);               // the sequence's rows of this block
           const int steps = (min(kKeys, seen - i * kKeys) + 15) / 16;  // 16-key steps that some token sees
           if (live < 16 * steps) {
@@ -507,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_proxy_async();
             __syncwarp();
           }
-          if (!tc::mbar_wait(p_full + 2 * t + h, uses[h] & 1, status, 58, abort) ||
-              (i == 0 && !tc::mbar_wait(o_free + t, (units & 1) ^ 1, status, 59, abort))) {
+          if ((i == 0 && !tc::mbar_wait(o_free + t, units ^ 1, status, 59, abort)) ||
+              !tc::mbar_wait(p_full + 2 * t + h, uses[h], status, 58, abort)) {
             ok = false;
             break;
           }
-          ++uses[h];
+          uses[h] ^= 1;
           tc::tc_fence_after();
           const uint64_t vd = v_desc0 + ((sl * C::slot) >> 4);
 #pragma unroll
@@ -520,13 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kk < steps) mma_ts(leader, tO, tS + kKeys * h + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, i != 0 || kk != 0);
           commit(leader, pv_done + t);
           commit(leader, kv_empty + sl);
-          if (i + 2 < nb && !issue_s(i + 2)) { ok = false; break; }
+          if (i + 2 < nb) issue_s(i + 2, sk);
         }
         // what is left of the item is the other unit's
         if (ok && !pass(used)) ok = false;
-        g0 += used;
-        ++qn;
-        units += nb > 0;
+        qn = qn + 1 == C::qbufs ? 0 : qn + 1;
+        q_phase ^= qn == 0;
+        units ^= nb > 0;
       }
       commit(leader, done);
       tc::mbar_wait(done, 0, status, 60, abort);
