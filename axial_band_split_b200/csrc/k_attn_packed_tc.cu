@@ -6,7 +6,7 @@
 // Tiles.  The G = heads / kv_heads query heads that share a key head are rows of one matrix: a tile
 // is TQ = 128 / G tokens x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
 // box per 64 dimensions), so each key block is read once for all of them and a single new token
-// already fills G rows.  Key blocks are 64 rows.
+// already fills G rows.  Key blocks are 128 rows.
 //
 // Work items.  A CTA runs two units (a tile with a range of keys) t = 0, 1 side by side:
 //   pair   - two neighbouring tiles of one sequence and key head: they share every key block;
@@ -22,15 +22,15 @@
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, one score row per thread; warp 8: bulk tensor loads;
 // warps 9, 10: matrix instructions of unit 0, 1; warp 11: items.
 //
-// Places.  The scores of a unit's key blocks take turns in two places of 64 columns in tensor memory
-// (S_t at 128 t; O_t at 256), and the 16-bit probabilities P overwrite the scores they came from: the
-// softmax reads block i into registers, writes P(i), the issuer queues P(i) V and behind it, in the
-// tensor core's own order, the scores of block i + 2 into the same place.  So while the matrix
-// instructions of one block run, the softmax works on the other, and with both units the exponentials
-// rarely wait for a chain of products.
+// Tensor memory (512 columns).  With v up to 64 wide: S_t at 128 t, O_t at 256 + 64 t, P_t (the 16-bit
+// probabilities, half as wide) at 384 + 64 t, and the next block's scores compute under this block's
+// exponentials.  With wider v (S_t at 128 t, O_t at 256 + 128 t) P_t overwrites S_t once the softmax has
+// read it, and the issuer queues the next block's scores right behind P V, which the tensor core runs
+// in order; the two units then take turns, one's products under the other's exponentials.  P is handed
+// over in two halves of 64 keys, so P V of the first runs under the second's exponentials.
 //
-// K and V blocks stream through one ring in the order of their use, K0 K1 V0 K2 V1 ... (separate keys:
-// the two units' streams take turns).  Both issuers acknowledge every slot, their own when its reads have ended and
+// K and V blocks stream through one ring in the order of their use (separate keys: the two units'
+// streams take turns).  Both issuers acknowledge every slot, their own when its reads have ended and
 // the other unit's as it arrives: a phase of a slot's barrier is then never more than one ahead of
 // anybody who waits on it by parity.
 //
@@ -48,11 +48,11 @@
 namespace mrf {
 namespace {
 
-constexpr int kRows = 128, kKeys = 64;
-constexpr int kAtom = kRows * 128, kKAtom = kKeys * 128;  // 64 16-bit values of a tile's or a key block's rows
+constexpr int kRows = 128, kKeys = 128, kHalf = 64;
+constexpr int kAtom = kRows * 128;  // 64 16-bit values of 128 rows
 constexpr int kThreads = 384;
-// register split, as in the model's attention: 2 * 128 * 208 + 128 * 72 <= 384 * 168
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
+// register split, as in the model's attention: 2 * 128 * 200 + 128 * 96 <= 384 * 168
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsIo = 96;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
 constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
 constexpr int kItems = 4;            // ring of work items
@@ -75,8 +75,9 @@ struct Item {
 template <int QA, int VA>
 struct Cfg {
   static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
-  static constexpr int slot = (QA > VA ? QA : VA) * kKAtom;
-  static constexpr int slots = slot > kKAtom ? 10 : 16;  // ring of K or V blocks
+  static constexpr bool overlay = VA == 2;           // P over S
+  static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
+  static constexpr int slots = 10 * kAtom / slot;    // ring of K or V blocks
   static constexpr int q = 0;
   static constexpr int kv = 4 * kAtom;
   static constexpr int bar = kv + slots * slot;
@@ -146,6 +147,22 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                "r"(d)
                : "memory");
 }
+// 8 columns of this thread's lane times f (few registers: scores are held while it runs)
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Matrix instructions of a whole warp, issued by its `leader` lane alone: without a branch around them
@@ -185,7 +202,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // V as the MN-major B operand: 64-wide atoms side by side (the leading offset), 8 keys each 1024 bytes
 // (the stride offset).
 __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kKAtom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kAtom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
@@ -260,20 +277,23 @@ __device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
   return it;
 }
 
-// A stream of n key blocks in the order of its use: K0 K1 V0 K2 V1 ... V(n - 1).  The elements of block j.
-__device__ __forceinline__ int k_elem(int j) { return max(0, 2 * j - 1); }
-__device__ __forceinline__ int v_elem(int j, int n) { return min(2 * j + 2, 2 * n - 1); }
+// A stream of n key blocks in the order of its use, the elements of block j: with P over S K0 V0 K1 V1 ...,
+// else K0 K1 V0 K2 V1 ... V(n - 1).
+template <bool kOverlay>
+__device__ __forceinline__ int k_elem(int j) { return kOverlay ? 2 * j : max(0, 2 * j - 1); }
+template <bool kOverlay>
+__device__ __forceinline__ int v_elem(int j, int n) { return kOverlay ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
 
 // ------------------------------------------------------------------ softmax of one key block
 __device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
-  float ma = s[0], mb = s[16], mc = s[32], md = s[48];
+  float ma = s[0], mb = s[32], mc = s[64], md = s[96];
 #pragma unroll
-  for (int i = 1; i < 16; i += 2) {
-    const int i2 = i + 1 < 16 ? i + 1 : i;
+  for (int i = 1; i < 32; i += 2) {
+    const int i2 = i + 1 < 32 ? i + 1 : i;
     ma = max3(ma, s[i], s[i2]);
-    mb = max3(mb, s[16 + i], s[16 + i2]);
-    mc = max3(mc, s[32 + i], s[32 + i2]);
-    md = max3(md, s[48 + i], s[48 + i2]);
+    mb = max3(mb, s[32 + i], s[32 + i2]);
+    mc = max3(mc, s[64 + i], s[64 + i2]);
+    md = max3(md, s[96 + i], s[96 + i2]);
   }
   return fmaxf(fmaxf(ma, mb), fmaxf(mc, md));
 }
@@ -288,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bar);
   uint64_t *q_full = bars, *q_empty = bars + 2;          // [qbufs]
-  uint64_t *s_full = bars + 4, *p_full = bars + 8;       // [2 t + place]
+  uint64_t *s_full = bars + 4, *s_free = bars + 6;       // [2]: scores written / read (not with P over S)
+  uint64_t *p_full = bars + 8;                           // [2 t + half]
   uint64_t *pv_done = bars + 12, *o_free = bars + 14;    // [2]
   uint64_t *item_full = bars + 16, *item_empty = bars + 20;  // [kItems]
   uint64_t *done = bars + 24;
@@ -304,8 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     for (int b = 0; b < C::qbufs; ++b) { tc::mbar_init(q_full + b, 1); tc::mbar_init(q_empty + b, 2); }
     for (int s = 0; s < C::slots; ++s) { tc::mbar_init(kv_full + s, 1); tc::mbar_init(kv_empty + s, 2); }
-    for (int i = 0; i < 4; ++i) { tc::mbar_init(s_full + i, 1); tc::mbar_init(p_full + i, 4); }
-    for (int t = 0; t < 2; ++t) { tc::mbar_init(pv_done + t, 1); tc::mbar_init(o_free + t, 4); }
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(s_full + t, 1);
+      tc::mbar_init(s_free + t, 4);
+      tc::mbar_init(p_full + 2 * t, 4);
+      tc::mbar_init(p_full + 2 * t + 1, 4);
+      tc::mbar_init(pv_done + t, 1);
+      tc::mbar_init(o_free + t, 4);
+    }
     for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 11); }
     tc::mbar_init(done, 2);
     tc::fence_barrier_init();
@@ -401,12 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto fill = [&](int t, int e, int nb) {
             const int s = g % C::slots;
             if (!tc::mbar_wait(kv_empty + s, ((g / C::slots) & 1) ^ 1, status, 53, abort)) return false;
-            const bool is_k = e == 0 || ((e & 1) && e != 2 * nb - 1);
-            const int j = is_k ? (e + 1) / 2 : e == 2 * nb - 1 ? nb - 1 : e / 2 - 1, atoms = is_k ? QA : VA;
-            tc::mbar_arrive_expect_tx(kv_full + s, atoms * kKAtom);
+            const bool is_k = C::overlay ? !(e & 1) : e == 0 || ((e & 1) && e != 2 * nb - 1);
+            const int j = C::overlay ? e / 2 : is_k ? (e + 1) / 2 : e == 2 * nb - 1 ? nb - 1 : e / 2 - 1;
+            const int atoms = is_k ? QA : VA;
+            // a range's last block of up to 64 keys loads no more
+            const int halves = it.u[t].klen - j * kKeys > kHalf ? 2 : 1;
+            tc::mbar_arrive_expect_tx(kv_full + s, atoms * halves * (kAtom / 2));
             for (int c = 0; c < atoms; ++c)
-              tc::tma_load_3d(smem + C::kv + s * C::slot + c * kKAtom, is_k ? &tk : &tv, kv_full + s, 64 * c, it.u[t].kvh,
-                              it.u[t].k_row + j * kKeys);
+              for (int h = 0; h < halves; ++h)
+                tc::tma_load_3d(smem + C::kv + s * C::slot + c * kAtom + h * (kAtom / 2), is_k ? &tk : &tv, kv_full + s, 64 * c,
+                                it.u[t].kvh, it.u[t].k_row + j * kKeys + h * kHalf);
             ++g;
             return true;
           };
@@ -428,12 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = uniform(warp - 9);
       const uint32_t leader = elect_lane();
       Item it;
-      const uint32_t id_s = tc::idesc_f16(kRows, kKeys, false, kBF);
+      const uint32_t id_s = tc::idesc_f16(kRows, kKeys, false, kBF), id_s64 = tc::idesc_f16(kRows, kHalf, false, kBF);
       const uint32_t id_pv = tc::idesc_f16(kRows, (a.v_width + 15) / 16 * 16, true, kBF);
       const int qk_steps = (a.width + 15) / 16;
       const uint32_t tS = tmem + 128 * t, tO = tmem + kOCol + kOStep * t;
+      const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
       int ring = 0, qn = 0;             // next ring slot, q buffer
-      uint32_t ring_phase = 0, q_phase = 0, units = 0, uses[2] = {0, 0};  // parities: of those, of units, of the places' uses
+      uint32_t ring_phase = 0, q_phase = 0, units = 0, blocks = 0;  // parities: of those, and of this unit's
       // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
       // / 16, below 2^14 within shared memory)
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * QA * kAtom);
@@ -476,58 +508,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance();
           return sl;
         };
-        // scores of block i, into the place that P(i - 2) V, queued before, reads
-        auto issue_s = [&](int i, int sl) {
-          const int h = i & 1;
+        // scores of block j (with P over S: over the P that P V, queued before, reads)
+        auto issue_s = [&](int j, int sl) {
           tc::tc_fence_after();
+          const uint32_t id = klen - j * kKeys > kHalf ? id_s : id_s64;
           const uint64_t qd = q_desc + ((qn * 2 * QA * kAtom) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4 * QA; ++kk)
             if (kk < qk_steps)
-              mma_ss(leader, tS + kKeys * h, qd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
-                     kd + (((kk / 4) * kKAtom + (kk % 4) * 32) >> 4), id_s, kk != 0);
-          commit(leader, s_full + 2 * t + h);
+              mma_ss(leader, tS, qd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
+                     kd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4), id, kk != 0);
+          commit(leader, s_full + t);
           commit(leader, kv_empty + sl);
-          if (i == nb - 1) commit(leader, q_empty + qn);
+          if (j == nb - 1) commit(leader, q_empty + qn);
         };
         if (!tc::mbar_wait(q_full + qn, q_phase, status, 55, abort)) { ok = false; break; }
         if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qn);
-        for (int i = 0; ok && i < min(nb, 2); ++i) {
-          const int sl = take(k_elem(i));
-          if (sl < 0) ok = false;
-          else issue_s(i, sl);
+        if (nb > 0) {
+          const int sk = take(k_elem<C::overlay>(0));
+          // (S_t was read by the previous unit's last softmax: its P V has been queued)
+          if (sk < 0) { ok = false; break; }
+          issue_s(0, sk);
         }
-        if (!ok) break;
-        for (int i = 0; i < nb; ++i) {
-          const int h = i & 1, sl = take(v_elem(i, all));
-          const int sk = i + 2 < nb && sl >= 0 ? take(k_elem(i + 2)) : 0;  // ahead of the wait for P(i)
+        for (int j = 0; j < nb; ++j) {
+          int sk = 0, sl = 0;
+          if (!C::overlay && j + 1 < nb) {
+            sk = take(k_elem<false>(j + 1));
+            if (sk < 0 || !tc::mbar_wait(s_free + t, blocks, status, 57, abort)) { ok = false; break; }
+            issue_s(j + 1, sk);
+          }
+          sl = take(v_elem<C::overlay>(j, all));
+          if (C::overlay && sl >= 0 && j + 1 < nb) sk = take(k_elem<true>(j + 1));  // ahead of the wait for P
           if (sl < 0 || sk < 0) { ok = false; break; }
-          const int live = min(kKeys, klen - i * kKeys);               // the sequence's rows of this block
-          const int steps = (min(kKeys, seen - i * kKeys) + 15) / 16;  // 16-key steps that some token sees
+          const int live = min(kKeys, klen - j * kKeys);               // the range's rows of this block
+          const int steps = (min(kKeys, seen - j * kKeys) + 15) / 16;  // 16-key steps that some token sees
           if (live < 16 * steps) {
             // rows of no sequence: zeros, whatever they hold (both units of a pair write the same zeros)
             uint8_t *vs = smem + C::kv + sl * C::slot;
             const int rows = 16 * steps - live;
             for (int c = lane; c < rows * 8 * VA; c += 32)
-              *reinterpret_cast<uint4 *>(vs + (c / (rows * 8)) * kKAtom + (live + (c / 8) % rows) * 128 + (c % 8) * 16) =
+              *reinterpret_cast<uint4 *>(vs + (c / (rows * 8)) * kAtom + (live + (c / 8) % rows) * 128 + (c % 8) * 16) =
                   make_uint4(0, 0, 0, 0);
             tc::fence_proxy_async();
             __syncwarp();
           }
-          if ((i == 0 && !tc::mbar_wait(o_free + t, units ^ 1, status, 59, abort)) ||
-              !tc::mbar_wait(p_full + 2 * t + h, uses[h], status, 58, abort)) {
+          const uint64_t vd = v_desc0 + ((sl * C::slot) >> 4);
+          if ((j == 0 && !tc::mbar_wait(o_free + t, units ^ 1, status, 59, abort)) ||
+              !tc::mbar_wait(p_full + 2 * t, blocks, status, 58, abort)) {
             ok = false;
             break;
           }
-          uses[h] ^= 1;
           tc::tc_fence_after();
-          const uint64_t vd = v_desc0 + ((sl * C::slot) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            if (kk < steps) mma_ts(leader, tO, tS + kKeys * h + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, i != 0 || kk != 0);
+            if (kk < steps) mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, j != 0 || kk != 0);
+          if (!tc::mbar_wait(p_full + 2 * t + 1, blocks, status, 58, abort)) { ok = false; break; }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            if (kk < steps) mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, 1);
           commit(leader, pv_done + t);
           commit(leader, kv_empty + sl);
-          if (i + 2 < nb) issue_s(i + 2, sk);
+          blocks ^= 1;
+          if (C::overlay && j + 1 < nb) issue_s(j + 1, sk);
         }
         // what is left of the item is the other unit's
         if (ok && !pass(used)) ok = false;
@@ -546,8 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = r / a.G, head = r - tok * a.G;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + kOCol + kOStep * t + lane_off;
+    const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t + lane_off;
     const float c = a.scale_log2;
-    uint32_t uses[2] = {0, 0}, steps = 0;  // of each place, and blocks in all
+    uint32_t blocks = 0;  // of this unit in all
     Item it;
     for (int n = 0; next_item(n, it); ++n) {
       const int nb = it.u[t].nblk;
@@ -557,86 +601,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis = row ? max(0, min(it.u[t].klen, it.u[t].lim0 + tok)) : 0x7fffffff;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int i = 0; i < nb; ++i, ++steps) {
-        const int h = i & 1;
-        // (these scores also say that P(i - 2) V has ended: the tensor core works in order)
-        if (!tc::mbar_wait(s_full + 2 * t + h, uses[h] & 1, status, 61, abort)) { ok = false; break; }
-        ++uses[h];
+      for (int j = 0; j < nb; ++j, ++blocks) {
+        // (with P over S these scores also say that the block before's P V has ended: the tensor core
+        // works in order)
+        if (!tc::mbar_wait(s_full + t, blocks & 1, status, 61, abort)) { ok = false; break; }
         tc::tc_fence_after();
-        if (live) {
-          float sv[kKeys];
-          {
-            uint32_t raw[kKeys];
-#pragma unroll
-            for (int k = 0; k < kKeys; k += 32) tmem_ld32_async(tS + kKeys * h + k, raw + k);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < kKeys; k += 32) tmem_landed(raw + k);
-#pragma unroll
-            for (int k = 0; k < kKeys; ++k) sv[k] = __uint_as_float(raw[k]);
+        if (!live) {
+          // its arrival for this block must not count for the one before: that block's P V has ended
+          if (!C::overlay && lane == 0) tc::mbar_arrive(s_free + t);
+          if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort)) { ok = false; break; }
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(p_full + 2 * t);
+            tc::mbar_arrive(p_full + 2 * t + 1);
           }
-          const int hi = vis - i * kKeys;
-          if (__any_sync(0xffffffffu, hi < kKeys)) {
+          continue;
+        }
+        float sv[kKeys];
+        {
+          uint32_t raw[kKeys];
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
-              if (k >= hi) sv[k] = -INFINITY;
-          }
-          const float bm = row_max(sv);
-          bool need = false;
-          float alpha = 1.f;
-          if (i == 0) {
+          for (int k = 0; k < kKeys; k += 32) tmem_ld32_async(tS + k, raw + k);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kKeys; k += 32) tmem_landed(raw + k);
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k) sv[k] = __uint_as_float(raw[k]);
+        }
+        if (!C::overlay) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(s_free + t);
+        }
+        const int hi = vis - j * kKeys;
+        if (__any_sync(0xffffffffu, hi < kKeys)) {
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k)
+            if (k >= hi) sv[k] = -INFINITY;
+        }
+        const float bm = row_max(sv);
+        bool need = false;
+        float alpha = 1.f;
+        if (j == 0) {
+          m = bm;
+        } else {
+          need = row && (bm - m) * c > kRescaleLog2;  // also from -inf, whose l and O are zero
+          if (need) {
+            alpha = ex2((m - bm) * c);
+            l *= alpha;
             m = bm;
-          } else {
-            need = row && (bm - m) * c > kRescaleLog2;  // also from -inf, whose l and O are zero
-            if (need) {
-              alpha = ex2((m - bm) * c);
-              l *= alpha;
-              m = bm;
-            }
           }
-          // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
-          const float negm = m == -INFINITY ? 0.f : -m * c;
-          const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
-          uint32_t pk[kKeys / 2];
-          float2 sum[4] = {};
+        }
+        // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
+        const float negm = m == -INFINITY ? 0.f : -m * c;
+        const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
+        float2 sum[4] = {};
 #pragma unroll
-          for (int k = 0; k < kKeys; k += 8) {
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[kHalf / 2];
+#pragma unroll
+          for (int k = 0; k < kHalf; k += 8) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const float2 d = __ffma2_rn(make_float2(sv[k + 2 * u], sv[k + 2 * u + 1]), c2, n2);
+              const float2 d = __ffma2_rn(make_float2(sv[half * kHalf + k + 2 * u], sv[half * kHalf + k + 2 * u + 1]), c2, n2);
               const float2 p = make_float2(ex2(d.x), ex2(d.y));
               sum[u] = __fadd2_rn(sum[u], p);
               pk[(k >> 1) + u] = pack2<kBF>(p.x, p.y);
             }
           }
-          const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-          l += s4.x + s4.y;
-#pragma unroll
-          for (int k = 0; k < kKeys / 2; k += 4) tmem_st4(tS + kKeys * h + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
-          tmem_wait_st();
-          if (__any_sync(0xffffffffu, need)) {
-            // O_t moves to the new maximum once P(i - 1) V has ended
-            if (!tc::mbar_wait(pv_done + t, (steps - 1) & 1, status, 62, abort)) { ok = false; break; }
+          if (half == 0) {
+            // P_t and O_t are free once the previous block's P V has ended
+            if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort)) { ok = false; break; }
             tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 64 * VA; k += 32) {
-              float v[32];
-              tc::tmem_ld32(tO + k, v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= alpha;
-              tc::tmem_st32(tO + k, v);
-            }
           }
+#pragma unroll
+          for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + half * (kHalf / 2) + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
+          if (half == 0 && __any_sync(0xffffffffu, need)) {  // O_t moves to the new maximum
+#pragma unroll
+            for (int k = 0; k < 64 * VA; k += 8) tmem_scale8(tO + k, alpha);
+          }
+          tmem_wait_st();
           tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(p_full + 2 * t + half);
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + 2 * t + h);
+        if (!ok) break;
+        const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+        l += s4.x + s4.y;
       }
       if (!ok) break;
       if (nb > 0) {
-        // the last product; first the one before it, so that one phase at most is outstanding
-        if (nb > 1 && !tc::mbar_wait(pv_done + t, (steps - 2) & 1, status, 63, abort)) break;
-        if (!tc::mbar_wait(pv_done + t, (steps - 1) & 1, status, 63, abort)) break;
+        if (!tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 63, abort)) break;
         tc::tc_fence_after();
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that saw no key: zeros
@@ -833,7 +888,7 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   const ull kst[2] = {st1(m.kv_heads, m.k_head_stride, m.width), st1(m.k_rows, m.k_token_stride, m.width)};
   const ull vd[3] = {(ull)m.v_width, (ull)m.kv_heads, (ull)m.k_rows};
   const ull vst[2] = {st1(m.kv_heads, m.v_head_stride, m.v_width), st1(m.k_rows, m.v_token_stride, m.v_width)};
-  const unsigned qbox[4] = {64, (unsigned)a.G, 1, (unsigned)a.TQ}, kbox[3] = {64, 1, kKeys};
+  const unsigned qbox[4] = {64, (unsigned)a.G, 1, (unsigned)a.TQ}, kbox[3] = {64, 1, kHalf};
   CUtensorMap tq, tk, tv;
   if (!make_tmap(&tq, m.q, kTmF16, 4, qd, qst, qbox, 128) || !make_tmap(&tk, m.k, kTmF16, 3, kd, kst, kbox, 128) ||
       !make_tmap(&tv, m.v, kTmF16, 3, vd, vst, kbox, 128))
