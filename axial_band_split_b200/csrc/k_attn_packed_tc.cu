@@ -12,10 +12,11 @@
 //   pair   - two neighbouring tiles of one sequence and key head: they share every key block;
 //   heads  - a sequence's odd tile (its first, which sees the fewest keys) for two key heads, each
 //            unit with its own keys: short prompts and single tokens have nothing but these;
-//   splits - with few tiles and long keys, two key ranges of one tile: every range leaves its own
-//            output and log-sum in the workspace, and combine_kernel joins them.
-// Items are numbered sequence by sequence, a causal sequence's last tiles (the most keys) first, and
-// taken round robin by persistent CTAs.  Lengths live in device memory, so warp 11 finds each item's
+//   splits - with few tiles and long keys, two key ranges of one tile: the ranges, of equal size in all
+//            sequences, leave their own outputs and log-sums in the workspace, and combine_kernel joins them.
+// Items are numbered sequence by sequence, a causal sequence's last tiles (the most keys) first.  The grid
+// has a block for each; a running CTA takes over blocks that have not been launched (cluster launch
+// control), so that items go to whoever is free, in order.  Lengths live in device memory, so warp 11 finds each item's
 // sequence by a running prefix sum over the sequences' item counts and hands it to the others
 // through a ring in shared memory.
 //
@@ -24,10 +25,12 @@
 //
 // Tensor memory (512 columns).  With v up to 64 wide: S_t at 128 t, O_t at 256 + 64 t, P_t (the 16-bit
 // probabilities, half as wide) at 384 + 64 t, and the next block's scores compute under this block's
-// exponentials.  With wider v (S_t at 128 t, O_t at 256 + 128 t) P_t overwrites S_t once the softmax has
-// read it, and the issuer queues the next block's scores right behind P V, which the tensor core runs
-// in order; the two units then take turns, one's products under the other's exponentials.  P is handed
-// over in two halves of 64 keys, so P V of the first runs under the second's exponentials.
+// exponentials.  With wider v S_t at 128 t and O_t at 256 + 128 t fill it.  P is handed over in two
+// halves of 64 keys, so P V of the first runs under the second's exponentials; with wider v the first
+// half overwrites S_t (the softmax has read it all), the second goes through shared memory, and the
+// issuer queues the next block's scores right behind the first half's P V, which the tensor core runs in
+// order: they are ready when the second half's exponentials are done.  (With both halves over S_t they
+// had to wait for the whole P V, about 1200 of a block's 4000 clk.)
 //
 // K and V blocks stream through one ring in the order of their use (separate keys: the two units'
 // streams take turns).  Both issuers acknowledge every slot, their own when its reads have ended and
@@ -49,13 +52,14 @@ namespace mrf {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128, kHalf = 64;
+constexpr int kLate = 32;           // keys of P's second half whose exponentials run before the first half is handed over
 constexpr int kAtom = kRows * 128;  // 64 16-bit values of 128 rows
 constexpr int kThreads = 384;
 // register split, as in the model's attention: 2 * 128 * 200 + 128 * 96 <= 384 * 168
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsIo = 96;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
 constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
-constexpr int kItems = 4;            // ring of work items
+constexpr int kItems = 1;            // ring of work items: the next one is taken when everybody has begun this one
 
 // One unit of an item.  Token i of the tile sees the first min(klen, lim0 + i) keys of its range.
 struct Unit {
@@ -69,20 +73,23 @@ struct Unit {
 struct Item {
   Unit u[2];
   int shared;  // both units read the same key blocks
+  int partial; // one key range of several: outputs go to the workspace
   int last;    // no more items
 };
 
 template <int QA, int VA>
 struct Cfg {
   static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
-  static constexpr bool overlay = VA == 2;           // P over S
+  static constexpr bool overlay = VA == 2;           // P's first half over S, its second in shared memory
   static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
-  static constexpr int slots = 10 * kAtom / slot;    // ring of K or V blocks
+  static constexpr int slots = (overlay ? 8 : 10) * kAtom / slot;  // ring of K or V blocks
   static constexpr int q = 0;
   static constexpr int kv = 4 * kAtom;
-  static constexpr int bar = kv + slots * slot;
+  static constexpr int p = kv + slots * slot;        // [2 units] the second half of P
+  static constexpr int bar = p + (overlay ? 2 * kAtom : 0);
   static constexpr int item = bar + 512;
-  static constexpr int total = item + kItems * (int)sizeof(Item) + 16;
+  static constexpr int resp = (item + kItems * (int)sizeof(Item) + 15) / 16 * 16;  // taken_block's answer
+  static constexpr int total = resp + 16;
 };
 static_assert(Cfg<1, 1>::total + 1024 <= 232448 && Cfg<2, 2>::total + 1024 <= 232448 && Cfg<2, 1>::total + 1024 <= 232448 &&
                   Cfg<1, 2>::total + 1024 <= 232448,
@@ -95,9 +102,33 @@ struct Args {
   float *part_lse;
   const int32_t *q_offsets, *k_start, *k_len;
   long long out_token_stride, out_head_stride;
-  int q_rows, k_rows, seqs, heads, kv_heads, G, TQ, width, v_width, causal, splits;
+  int q_rows, k_rows, seqs, heads, kv_heads, G, TQ, width, v_width, causal;
+  int chunk, max_splits;  // keys of a range (0: no splits), ranges that the workspace holds
   float scale, scale_log2;
 };
+
+// Take over the next block of the grid that has not been launched: the answer arrives at resp (16 bytes) and
+// counts on bar.
+__device__ __forceinline__ void take_block(void *resp, uint64_t *bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   tc::smem_u32(resp)),
+               "r"(tc::smem_u32(bar))
+               : "memory");
+}
+// Its index, or -1 when there was none left (nobody may ask again then).
+__device__ __forceinline__ int taken_block(const void *resp) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x)
+      : "r"(tc::smem_u32(resp))
+      : "memory");
+  return x;
+}
 
 __device__ unsigned g_status[2];  // a bounded wait that expired: 1, site
 
@@ -231,16 +262,24 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int b) {
   }
   return s;
 }
-__device__ __forceinline__ int seq_items(const Args &a, int nq) {
-  const int nt = (nq + a.TQ - 1) / a.TQ;
-  if (a.splits > 1) return nt * a.kv_heads * (a.splits / 2);
-  return a.kv_heads * (nt / 2) + (nt & 1) * ((a.kv_heads + 1) / 2);
+// The keys of a sequence's ranges: whole blocks, more of them than `chunk` only where the workspace would not
+// hold the ranges (max_k was too low).
+__device__ __forceinline__ int range_keys(const Args &a, int nk) {
+  if (a.chunk == 0) return nk;
+  const int least = ((nk + a.max_splits - 1) / a.max_splits + kKeys - 1) / kKeys * kKeys;
+  return max(a.chunk, least);
+}
+__device__ __forceinline__ int range_count(const Args &a, int nk) {
+  return a.chunk == 0 ? 1 : max(1, (nk - 1) / range_keys(a, nk) + 1);
+}
+__device__ __forceinline__ long long seq_items(const Args &a, const Seq &s) {
+  const int nt = (s.nq + a.TQ - 1) / a.TQ, ns = range_count(a, s.nk);
+  if (ns > 1) return (long long)nt * a.kv_heads * ((ns + 1) / 2);
+  return (long long)a.kv_heads * (nt / 2) + (nt & 1) * ((a.kv_heads + 1) / 2);
 }
 __device__ __forceinline__ Unit make_unit(const Args &a, const Seq &s, int tile, int kvh, int split) {
   Unit u;
-  const int t0 = tile * a.TQ;
-  // a split's keys: whole blocks, the last one what is left
-  const int chunk = a.splits > 1 ? ((s.nk + a.splits - 1) / a.splits + kKeys - 1) / kKeys * kKeys : s.nk;
+  const int t0 = tile * a.TQ, chunk = range_keys(a, s.nk);
   const int r0 = (int)min((long long)split * chunk, (long long)s.nk);
   u.q_row = s.q0 + t0;
   u.ntok = min(a.TQ, s.nq - t0);
@@ -252,23 +291,25 @@ __device__ __forceinline__ Unit make_unit(const Args &a, const Seq &s, int tile,
   u.split = split;
   return u;
 }
-__device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
+__device__ __forceinline__ Item make_item(const Args &a, const Seq &s, long long r) {
   Item it;
-  const int nt = (s.nq + a.TQ - 1) / a.TQ;
+  const int nt = (s.nq + a.TQ - 1) / a.TQ, ns = range_count(a, s.nk);
   it.last = 0;
   it.shared = 0;
-  if (a.splits > 1) {
-    const int js = a.splits / 2, j = r % js, th = r / js;
+  it.partial = ns > 1;
+  if (ns > 1) {
+    const int js = (ns + 1) / 2, j = (int)(r % js), th = (int)(r / js);
     const int tile = nt - 1 - th / a.kv_heads, kvh = th % a.kv_heads;
     it.u[0] = make_unit(a, s, tile, kvh, 2 * j);
     it.u[1] = make_unit(a, s, tile, kvh, 2 * j + 1);
-  } else if (r < a.kv_heads * (nt / 2)) {
-    const int tile = (nt & 1) + 2 * (nt / 2 - 1 - r / a.kv_heads), kvh = r % a.kv_heads;
+    if (2 * j + 1 >= ns) it.u[1].ntok = it.u[1].nblk = 0;
+  } else if (r < (long long)a.kv_heads * (nt / 2)) {
+    const int tile = (nt & 1) + 2 * (nt / 2 - 1 - (int)(r / a.kv_heads)), kvh = (int)(r % a.kv_heads);
     it.shared = 1;
     it.u[0] = make_unit(a, s, tile, kvh, 0);
     it.u[1] = make_unit(a, s, tile + 1, kvh, 0);
   } else {
-    const int kvh = 2 * (r - a.kv_heads * (nt / 2));
+    const int kvh = 2 * (int)(r - (long long)a.kv_heads * (nt / 2));
     it.u[0] = make_unit(a, s, 0, kvh, 0);
     it.u[1] = it.u[0];
     it.u[1].kvh = kvh + 1;
@@ -277,7 +318,7 @@ __device__ __forceinline__ Item make_item(const Args &a, const Seq &s, int r) {
   return it;
 }
 
-// A stream of n key blocks in the order of its use, the elements of block j: with P over S K0 V0 K1 V1 ...,
+// A stream of n key blocks in the order of its use, the elements of block j: with wide v K0 V0 K1 V1 ...,
 // else K0 K1 V0 K2 V1 ... V(n - 1).
 template <bool kOverlay>
 __device__ __forceinline__ int k_elem(int j) { return kOverlay ? 2 * j : max(0, 2 * j - 1); }
@@ -285,19 +326,49 @@ template <bool kOverlay>
 __device__ __forceinline__ int v_elem(int j, int n) { return kOverlay ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
 
 // ------------------------------------------------------------------ softmax of one key block
-__device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
-  float ma = s[0], mb = s[32], mc = s[64], md = s[96];
+// This thread's row of scores from tensor memory, those at hi and past it -inf.
+__device__ __forceinline__ void load_scores(uint32_t tS, float (&s)[kKeys], bool masked, int hi) {
+  uint32_t raw[kKeys];
 #pragma unroll
-  for (int i = 1; i < 32; i += 2) {
-    const int i2 = i + 1 < 32 ? i + 1 : i;
-    ma = max3(ma, s[i], s[i2]);
-    mb = max3(mb, s[32 + i], s[32 + i2]);
-    mc = max3(mc, s[64 + i], s[64 + i2]);
-    md = max3(md, s[96 + i], s[96 + i2]);
+  for (int k = 0; k < kKeys; k += 32) tmem_ld32_async(tS + k, raw + k);
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < kKeys; k += 32) tmem_landed(raw + k);
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) s[k] = __uint_as_float(raw[k]);
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      if (k >= hi) s[k] = -INFINITY;
   }
-  return fmaxf(fmaxf(ma, mb), fmaxf(mc, md));
 }
 
+__device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
+  constexpr int n = 8;  // chains
+  float m[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) m[i] = s[i];
+#pragma unroll
+  for (int k = n; k < kKeys; k += 2 * n)
+#pragma unroll
+    for (int i = 0; i < n; ++i) m[i] = k + n + i < kKeys ? max3(m[i], s[k + i], s[k + n + i]) : fmaxf(m[i], s[k + i]);
+#pragma unroll
+  for (int i = 1; i < n; ++i) m[0] = fmaxf(m[0], m[i]);
+  return m[0];
+}
+
+// pk <- 2^(c s + negm) of the keys kA .. kB, two 16-bit values each, and their unrounded sums
+template <bool kBF, int kA, int kB>
+__device__ __forceinline__ void exponentials(const float (&s)[kKeys], float c, float negm, float2 (&sum)[4], uint32_t *pk) {
+  const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
+#pragma unroll
+  for (int k = kA; k < kB; k += 2) {
+    const float2 d = __ffma2_rn(make_float2(s[k], s[k + 1]), c2, n2);
+    const float2 p = make_float2(ex2(d.x), ex2(d.y));
+    sum[k / 2 % 4] = __fadd2_rn(sum[k / 2 % 4], p);
+    pk[(k - kA) / 2] = pack2<kBF>(p.x, p.y);
+  }
+}
 // ------------------------------------------------------------------ the kernel
 template <bool kBF, int QA, int VA>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -312,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *p_full = bars + 8;                           // [2 t + half]
   uint64_t *pv_done = bars + 12, *o_free = bars + 14;    // [2]
   uint64_t *item_full = bars + 16, *item_empty = bars + 20;  // [kItems]
-  uint64_t *done = bars + 24;
-  uint64_t *kv_full = bars + 25, *kv_empty = kv_full + C::slots;
-  static_assert(25 + 2 * C::slots <= 62, "barrier area");
+  uint64_t *done = bars + 24, *block_full = bars + 25;
+  uint64_t *kv_full = bars + 26, *kv_empty = kv_full + C::slots;
+  static_assert(26 + 2 * C::slots <= 62, "barrier area");
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 62);
   volatile int *abort = reinterpret_cast<int *>(bars + 63);
   Item *items = reinterpret_cast<Item *>(smem + C::item);
@@ -335,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 11); }
     tc::mbar_init(done, 2);
+    tc::mbar_init(block_full, 1);
     tc::fence_barrier_init();
   }
   if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
@@ -366,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long cnt = 0;
         if (base + lane < a.seqs) {
           s = load_seq(a, base + lane);
-          cnt = seq_items(a, s.nq);
+          cnt = seq_items(a, s);
         }
         incl = cnt;
         for (int o = 1; o < 32; o <<= 1) {
@@ -376,16 +448,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         total = __shfl_sync(0xffffffffu, incl, 31);
       };
       load();
-      int n = 0;
-      for (long long it = blockIdx.x;; it += gridDim.x, ++n) {
-        while (base < a.seqs && it >= before + total) {
-          base += 32;
-          before += total;
-          load();
-        }
-        const bool last = base >= a.seqs;
+      long long it = blockIdx.x;
+      for (int n = 0, asked = 0;; ++n) {
+        if (!tc::mbar_wait(item_empty + n % kItems, ((n / kItems) & 1) ^ 1, status, 51, abort)) break;
         Item item;
-        if (!last) {
+        item.last = 1;
+        // the next block that has an item (the grid may have more blocks than there are items: those are
+        // taken over too, and dropped)
+        for (bool first = n == 0; it >= 0 && item.last; first = false) {
+          if (!first) {
+            if (lane == 0) {
+              tc::fence_proxy_async();  // after the last answer was read
+              tc::mbar_arrive_expect_tx(block_full, 16);
+              take_block(smem + C::resp, block_full);
+            }
+            if (!tc::mbar_wait(block_full, asked & 1, status, 64, abort)) {
+              drain(block_full, asked & 1);
+              break;
+            }
+            ++asked;
+            it = taken_block(smem + C::resp);
+            __syncwarp();
+            if (it < 0) break;
+          }
+          while (base < a.seqs && it >= before + total) {
+            base += 32;
+            before += total;
+            load();
+          }
+          if (base >= a.seqs) continue;
           const long long r = it - before;
           const int src = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
           Seq q;
@@ -393,16 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           q.nq = __shfl_sync(0xffffffffu, s.nq, src);
           q.k0 = __shfl_sync(0xffffffffu, s.k0, src);
           q.nk = __shfl_sync(0xffffffffu, s.nk, src);
-          item = make_item(a, q, (int)(r - (__shfl_sync(0xffffffffu, incl, src) - seq_items(a, q.nq))));
+          item = make_item(a, q, r - (__shfl_sync(0xffffffffu, incl, src) - seq_items(a, q)));
         }
-        item.last = last;
-        if (!tc::mbar_wait(item_empty + n % kItems, ((n / kItems) & 1) ^ 1, status, 51, abort)) break;
         if (lane == 0) {
           items[n % kItems] = item;
           tc::mbar_arrive(item_full + n % kItems);
         }
         __syncwarp();
-        if (last) break;
+        if (item.last) break;
       }
     } else if (warp == 8) {
       // ---------------- bulk tensor loads
@@ -466,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
       int ring = 0, qn = 0;             // next ring slot, q buffer
       uint32_t ring_phase = 0, q_phase = 0, units = 0, blocks = 0;  // parities: of those, and of this unit's
+      const uint64_t p_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::p) + t * kAtom);
       // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
       // / 16, below 2^14 within shared memory)
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * QA * kAtom);
@@ -508,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance();
           return sl;
         };
-        // scores of block j (with P over S: over the P that P V, queued before, reads)
+        // scores of block j (with wide v over the half of P that P V, queued before, reads)
         auto issue_s = [&](int j, int sl) {
           tc::tc_fence_after();
           const uint32_t id = klen - j * kKeys > kHalf ? id_s : id_s64;
@@ -562,15 +652,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps) mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, j != 0 || kk != 0);
+          if (C::overlay && j + 1 < nb) issue_s(j + 1, sk);
           if (!tc::mbar_wait(p_full + 2 * t + 1, blocks, status, 58, abort)) { ok = false; break; }
           tc::tc_fence_after();
 #pragma unroll
           for (int kk = 4; kk < 8; ++kk)
-            if (kk < steps) mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, 1);
+            if (kk < steps) {
+              if (C::overlay) mma_ss(leader, tO, p_desc + (((kk - 4) * 32) >> 4), vd + ((kk * 2048) >> 4), id_pv, 1);
+              else mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, 1);
+            }
           commit(leader, pv_done + t);
           commit(leader, kv_empty + sl);
           blocks ^= 1;
-          if (C::overlay && j + 1 < nb) issue_s(j + 1, sk);
         }
         // what is left of the item is the other unit's
         if (ok && !pass(used)) ok = false;
@@ -599,17 +692,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = __any_sync(0xffffffffu, row);  // a warp without rows only keeps the barriers going
       // the keys this row sees (a row that is none needs no mask)
       const int vis = row ? max(0, min(it.u[t].klen, it.u[t].lim0 + tok)) : 0x7fffffff;
+      const int min_vis = __reduce_min_sync(0xffffffffu, vis);
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nb; ++j, ++blocks) {
-        // (with P over S these scores also say that the block before's P V has ended: the tensor core
-        // works in order)
         if (!tc::mbar_wait(s_full + t, blocks & 1, status, 61, abort)) { ok = false; break; }
         tc::tc_fence_after();
         if (!live) {
           // its arrival for this block must not count for the one before: that block's P V has ended
           if (!C::overlay && lane == 0) tc::mbar_arrive(s_free + t);
-          if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort)) { ok = false; break; }
+          if (j > 0 && !tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort)) { ok = false; break; }
           __syncwarp();
           if (lane == 0) {
             tc::mbar_arrive(p_full + 2 * t);
@@ -617,27 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        const int hi = vis - j * kKeys;
+        const bool masked = min_vis - j * kKeys < kKeys;
         float sv[kKeys];
-        {
-          uint32_t raw[kKeys];
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 32) tmem_ld32_async(tS + k, raw + k);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 32) tmem_landed(raw + k);
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k) sv[k] = __uint_as_float(raw[k]);
-        }
+        load_scores(tS, sv, masked, hi);
         if (!C::overlay) {
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(s_free + t);
-        }
-        const int hi = vis - j * kKeys;
-        if (__any_sync(0xffffffffu, hi < kKeys)) {
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k)
-            if (k >= hi) sv[k] = -INFINITY;
         }
         const float bm = row_max(sv);
         bool need = false;
@@ -652,40 +731,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = bm;
           }
         }
+        const bool any_need = __any_sync(0xffffffffu, need);
         // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
         const float negm = m == -INFINITY ? 0.f : -m * c;
-        const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
         float2 sum[4] = {};
+        uint32_t pk[kHalf / 2];
+        exponentials<kBF, 0, kHalf>(sv, c, negm, sum, pk);
+        // What P and O were used for before: with narrow v the previous block's P V read all of P_t; with
+        // wide v it read the second half's place, while the first half's is this block's own S_t.
+        auto previous_pv = [&]() { return j == 0 || tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort); };
+        if ((!C::overlay || any_need) && !previous_pv()) { ok = false; break; }
+        tc::tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[kHalf / 2];
+        for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
+        if (any_need) {  // O_t moves to the new maximum
 #pragma unroll
-          for (int k = 0; k < kHalf; k += 8) {
+          for (int k = 0; k < 64 * VA; k += 8) tmem_scale8(tO + k, alpha);
+        }
+        uint32_t pk1[kHalf / 2];
+        // (the store's latency under the second half's first exponentials)
+        exponentials<kBF, kHalf, kHalf + kLate>(sv, c, negm, sum, pk1);
+        tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 2 * t);
+        exponentials<kBF, kHalf + kLate, kKeys>(sv, c, negm, sum, pk1 + kLate / 2);
+        if (C::overlay) {
+          if (!previous_pv()) { ok = false; break; }
+          uint8_t *pr = smem + C::p + t * kAtom + r * 128;  // 128-byte rows of 64 keys, 16-byte chunk i of row r at i ^ (r % 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 d = __ffma2_rn(make_float2(sv[half * kHalf + k + 2 * u], sv[half * kHalf + k + 2 * u + 1]), c2, n2);
-              const float2 p = make_float2(ex2(d.x), ex2(d.y));
-              sum[u] = __fadd2_rn(sum[u], p);
-              pk[(k >> 1) + u] = pack2<kBF>(p.x, p.y);
-            }
-          }
-          if (half == 0) {
-            // P_t and O_t are free once the previous block's P V has ended
-            if (!C::overlay && j > 0 && !tc::mbar_wait(pv_done + t, (blocks - 1) & 1, status, 62, abort)) { ok = false; break; }
-            tc::tc_fence_after();
-          }
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(pr + ((k ^ (r & 7)) << 4)) = make_uint4(pk1[4 * k], pk1[4 * k + 1], pk1[4 * k + 2], pk1[4 * k + 3]);
+          tc::fence_proxy_async();
+        } else {
 #pragma unroll
-          for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + half * (kHalf / 2) + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
-          if (half == 0 && __any_sync(0xffffffffu, need)) {  // O_t moves to the new maximum
-#pragma unroll
-            for (int k = 0; k < 64 * VA; k += 8) tmem_scale8(tO + k, alpha);
-          }
+          for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + kHalf / 2 + k, pk1[k], pk1[k + 1], pk1[k + 2], pk1[k + 3]);
           tmem_wait_st();
           tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(p_full + 2 * t + half);
         }
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 2 * t + 1);
         const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
         l += s4.x + s4.y;
       }
@@ -704,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nb > 0) tc::tmem_ld32(tO + i, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = inv == 0.f ? 0.f : v[k] * inv;
-        if (row && a.splits > 1) {
+        if (row && it.partial) {
           float *o = a.part + (((long long)it.u[t].split * a.q_rows + at) * a.heads + h) * a.v_width + i;
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
@@ -725,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(o_free + t);
       }
       if (row) {
-        if (a.splits > 1)
+        if (it.partial)
           a.part_lse[((long long)it.u[t].split * a.q_rows + at) * a.heads + h] = l > 0.f || l != l ? m * c + log2f(l) : -INFINITY;
         else if (a.lse)
           a.lse[at * a.heads + h] = l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
@@ -740,15 +825,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the key ranges: one warp per (query row, head); weights 2^(L_s - max L) of the ranges' log2
-// sums, in the order of the ranges.
-template <bool kBF>
+// Joins the key ranges of the sequences that were split: kWarps warps a (query row, head), each taking every
+// kWarps-th range; weights 2^(L_s - max L) of the ranges' log2 sums, added in a fixed order.
+template <bool kBF, int kWarps>
 __global__ void __launch_bounds__(128) combine_kernel(const Args a) {
-  tc::griddep_wait();
-  const int lane = threadIdx.x & 31;
+  __shared__ float4 part[4][32];
+  __shared__ float weight[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long n = (long long)a.q_rows * a.heads;
-  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < n; i += gridDim.x * 4ll) {
-    const long long tok = i / a.heads;
+  constexpr int kRowsBlock = 4 / kWarps;
+  tc::griddep_wait();
+  for (long long i0 = (long long)blockIdx.x * kRowsBlock; i0 < n; i0 += (long long)gridDim.x * kRowsBlock) {
+    const long long i = i0 + warp / kWarps;
+    const long long tok = min(i, n - 1) / a.heads;
     int lo = 0, hi = a.seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -756,24 +845,48 @@ __global__ void __launch_bounds__(128) combine_kernel(const Args a) {
       else hi = mid;
     }
     const Seq s = load_seq(a, lo);
-    if (tok < s.q0 || tok >= s.q0 + s.nq) continue;  // a row of no sequence
-    float top = -INFINITY;
-    for (int k = 0; k < a.splits; ++k) top = fmaxf(top, a.part_lse[k * n + i]);
+    const int ns = range_count(a, s.nk);
+    const bool row = i < n && tok >= s.q0 && tok < s.q0 + s.nq && ns > 1;  // else of no sequence, or already written
+    float top = -INFINITY, total = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-    for (int k = 0; k < a.splits; ++k) {
-      const float ls = a.part_lse[k * n + i];
-      if (ls == -INFINITY) continue;
-      const float w = ex2(ls - top);
-      total += w;
-      if (4 * lane < a.v_width) {
-        const float4 p = *reinterpret_cast<const float4 *>(a.part + (k * n + i) * a.v_width + 4 * lane);
-        o.x = fmaf(w, p.x, o.x);
-        o.y = fmaf(w, p.y, o.y);
-        o.z = fmaf(w, p.z, o.z);
-        o.w = fmaf(w, p.w, o.w);
+    if (row) {
+      for (int k = lane; k < ns; k += 32) top = fmaxf(top, a.part_lse[k * n + i]);
+      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float base = top == -INFINITY ? 0.f : top;
+      for (int k0 = 0; k0 < ns; k0 += 32) {
+        const float mine = k0 + lane < ns ? a.part_lse[(k0 + lane) * n + i] : -INFINITY;
+        const float wl = mine == -INFINITY ? 0.f : ex2(mine - base);  // NaN stays
+        const int cnt = min(32, ns - k0);
+#pragma unroll 4
+        for (int k = warp % kWarps; k < cnt; k += kWarps) {
+          const float w = __shfl_sync(0xffffffffu, wl, k);
+          if (w != 0.f) {  // (a range without keys left no output)
+            total += w;
+            if (4 * lane < a.v_width) {
+              const float4 p = *reinterpret_cast<const float4 *>(a.part + ((k0 + k) * n + i) * a.v_width + 4 * lane);
+              o.x = fmaf(w, p.x, o.x);
+              o.y = fmaf(w, p.y, o.y);
+              o.z = fmaf(w, p.z, o.z);
+              o.w = fmaf(w, p.w, o.w);
+            }
+          }
+        }
       }
     }
+    if constexpr (kWarps > 1) {
+      __syncthreads();
+      part[warp][lane] = o;
+      if (lane == 0) weight[warp] = total;
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 4; ++w) {
+          const float4 p = part[w][lane];
+          o.x += p.x, o.y += p.y, o.z += p.z, o.w += p.w;
+          total += weight[w];
+        }
+      }
+    }
+    if (!row || warp % kWarps) continue;
     const bool any = total > 0.f || total != total;
     const float inv = any ? 1.f / total : 0.f;
     const long long h = i - tok * a.heads;
@@ -821,16 +934,29 @@ int sm_count() {
   return n;
 }
 
-// Key ranges a tile is split into (even, or 1): enough for two units on every SM when there are few
-// tiles, each range at least two key blocks.
-int split_count(const mrf_attention_args &a) {
+// How keys are split when there are few tiles: the keys of a range (0: no splits) and the most ranges a
+// sequence can have.
+struct Split {
+  int chunk, most;
+};
+Split split_of(const mrf_attention_args &a) {
   const int G = a.heads / a.kv_heads, TQ = kRows / G;
-  const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ);
-  const long long units = tiles * a.kv_heads, sms = sm_count();
-  const long long blocks = ((a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows) + kKeys - 1) / kKeys;
-  if (units > sms || blocks < 8) return 1;
-  const long long s = std::min<long long>({2 * (sms / units), blocks / 2, 128});
-  return s < 2 ? 1 : (int)(s & ~1ll);
+  const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ), units = tiles * a.kv_heads, sms = sm_count();
+  const long long keys = a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows, blocks = (keys + kKeys - 1) / kKeys;
+  // More units than SMs: only single tiles (new tokens) of sequences whose lengths only the device knows,
+  // where a long one would keep its SM while the others are done.
+  if (blocks < 8 || units > (tiles > a.seqs || a.seqs == 1 ? sms : 4 * sms)) return {0, 1};
+  // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
+  // about four rounds if all were as long as the longest; from 512 keys on a range's own cost (its
+  // queries, its output in fp32) is small.
+  const long long wanted = a.seqs == 1 ? 2 * (sms / units) : std::max(1ll, 8 * sms / units);
+  long long chunk = (blocks + std::max(1ll, wanted) - 1) / std::max(1ll, wanted);
+  chunk = std::max(chunk, a.seqs == 1 ? 2ll : 4ll);
+  chunk = std::max(chunk, (blocks + 127) / 128);
+  const long long most = (blocks + chunk - 1) / chunk;
+  // what the ranges write and read again in fp32 stays below half of the keys and values they read
+  if (most < 2 || most * a.q_rows * a.heads * a.v_width * 8 > units * keys * (a.width + a.v_width)) return {0, 1};
+  return {(int)(chunk * kKeys), (int)most};
 }
 
 bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
@@ -850,8 +976,8 @@ bool attention_tc_takes(const mrf_attention_args &a) {
 }
 
 size_t attention_tc_workspace(const mrf_attention_args &a) {
-  const int s = split_count(a);
-  return s > 1 ? (size_t)s * a.q_rows * a.heads * (a.v_width + 1) * sizeof(float) : 0;
+  const Split s = split_of(a);
+  return s.chunk ? (size_t)s.most * a.q_rows * a.heads * (a.v_width + 1) * sizeof(float) : 0;
 }
 
 bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cudaError_t *err) {
@@ -873,11 +999,13 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   a.width = m.width;
   a.v_width = m.v_width;
   a.causal = m.causal != 0;
-  a.splits = split_count(m);
+  const Split split = split_of(m);
+  a.chunk = split.chunk;
+  a.max_splits = split.most;
   a.scale = m.scale;
   a.scale_log2 = m.scale * 1.4426950408889634f;
   a.part = static_cast<float *>(m.workspace);
-  a.part_lse = a.part + (size_t)a.splits * a.q_rows * a.heads * a.v_width;
+  a.part_lse = a.part + (size_t)a.max_splits * a.q_rows * a.heads * a.v_width;
 
   // a dimension of one row needs no stride; the maps want a valid one
   auto st1 = [](long long n, long long s, int inner) { return (unsigned long long)(n <= 1 ? (inner + 7) / 8 * 8 : s); };
@@ -893,17 +1021,24 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   if (!make_tmap(&tq, m.q, kTmF16, 4, qd, qst, qbox, 128) || !make_tmap(&tk, m.k, kTmF16, 3, kd, kst, kbox, 128) ||
       !make_tmap(&tv, m.v, kTmF16, 3, vd, vst, kbox, 128))
     return false;
-  const long long tiles = (m.q_rows + a.TQ - 1) / a.TQ + m.seqs;
-  const int grid = (int)std::min<long long>(tiles * m.kv_heads * std::max(1, a.splits / 2), sm_count());
+  // At least a block for each item.  Without splits: with at most q_rows / TQ + seqs tiles, pairs of them
+  // for each key head and for every sequence's odd one half as many.  With splits, pairs of ranges.
+  const long long tiles = m.q_rows / a.TQ + m.seqs;
+  const long long items = a.chunk ? tiles * m.kv_heads * ((a.max_splits + 1) / 2)
+                                  : tiles / 2 * m.kv_heads + std::min<long long>(m.seqs, tiles) * ((m.kv_heads + 1) / 2);
+  const int grid = (int)std::max(1ll, items);
   const bool bf = m.dtype == MRF_DTYPE_BF16, q2 = m.width > 64, v2 = m.v_width > 64;
 #define MRF_ATTN(BF)                                                                                         \
   (q2 ? (v2 ? launch<BF, 2, 2>(tq, tk, tv, a, grid, st) : launch<BF, 2, 1>(tq, tk, tv, a, grid, st))         \
       : (v2 ? launch<BF, 1, 2>(tq, tk, tv, a, grid, st) : launch<BF, 1, 1>(tq, tk, tv, a, grid, st)))
   *err = bf ? MRF_ATTN(true) : MRF_ATTN(false);
 #undef MRF_ATTN
-  if (*err != cudaSuccess || a.splits == 1) return true;
+  if (*err != cudaSuccess || a.chunk == 0) return true;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>((m.q_rows * m.heads + 3) / 4, 148 * 16));
+  // many ranges: a block a row; few: a warp
+  const bool wide = a.max_splits > 8;
+  const long long rows = m.q_rows * m.heads;
+  cfg.gridDim = dim3((unsigned)std::min<long long>(wide ? rows : (rows + 3) / 4, 148 * 16));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -911,7 +1046,8 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  *err = bf ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a);
+  if (wide) *err = bf ? cudaLaunchKernelEx(&cfg, combine_kernel<true, 4>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<false, 4>, a);
+  else *err = bf ? cudaLaunchKernelEx(&cfg, combine_kernel<true, 1>, a) : cudaLaunchKernelEx(&cfg, combine_kernel<false, 1>, a);
   return true;
 }
 
