@@ -4,7 +4,7 @@
 // the SM.
 //
 // Tiles.  The G = heads / kv_heads query heads that share a key head are rows of one matrix: a tile
-// is TQ = 128 / G tokens x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
+// is TQ = 128 / G tokens (32 / G for single new tokens, see Cfg) x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
 // box per 64 dimensions), so each key block is read once for all of them and a single new token
 // already fills G rows.  Key blocks are 128 rows.
 //
@@ -77,23 +77,32 @@ struct Item {
   int last;    // no more items
 };
 
-template <int QA, int VA>
+// kFew: tiles of 32 rows (new tokens).  The matrix instructions still have 128 rows, but only 32 are stored:
+// unit t's are rows 32 t .. 32 t + 31 of an area of 64, which both units' operands start at, and what the
+// other rows read (the other unit's, the areas behind) ends in rows that nobody reads.  A unit's rows are one
+// warp's, on a scheduler of their own, and the room goes to more key blocks in flight.
+template <int QA, int VA, bool kFew>
 struct Cfg {
-  static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
   static constexpr bool overlay = VA == 2;           // P's first half over S, its second in shared memory
+  static constexpr int qbufs = QA == 1 ? 2 : 1;      // q buffers of two tiles
+  static constexpr int rows = kFew ? 32 : kRows;     // of a tile
+  static constexpr int tile = rows * 128;            // 64 16-bit values of a tile's rows
+  static constexpr int unit = kFew ? 0 : QA * kAtom; // from unit 0's q operand to unit 1's
+  static constexpr int step = kFew ? 2 * tile : kAtom;  // from one 64 values to the next
+  static constexpr int qbuf = 2 * QA * tile;
   static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
-  static constexpr int slots = (overlay ? 8 : 10) * kAtom / slot;  // ring of K or V blocks
   static constexpr int q = 0;
-  static constexpr int kv = 4 * kAtom;
-  static constexpr int p = kv + slots * slot;        // [2 units] the second half of P
-  static constexpr int bar = p + (overlay ? 2 * kAtom : 0);
+  static constexpr int p = q + qbufs * qbuf;         // the second half of P
+  static constexpr int kv = p + (overlay ? 2 * tile : 0);
+  static constexpr int slots = (14 * kAtom - kv) / slot;  // ring of K or V blocks
+  static constexpr int bar = kv + slots * slot;
   static constexpr int item = bar + 512;
   static constexpr int resp = (item + kItems * (int)sizeof(Item) + 15) / 16 * 16;  // taken_block's answer
   static constexpr int total = resp + 16;
+  static constexpr int warps = kFew ? 1 : 4;         // softmax warps of a unit
+  static_assert(total + 1024 <= 232448, "shared memory over the 227 KB limit");
+  static_assert(p + kAtom <= bar && q + qbufs * qbuf + kAtom <= bar, "operands of 128 rows stay inside");
 };
-static_assert(Cfg<1, 1>::total + 1024 <= 232448 && Cfg<2, 2>::total + 1024 <= 232448 && Cfg<2, 1>::total + 1024 <= 232448 &&
-                  Cfg<1, 2>::total + 1024 <= 232448,
-              "shared memory over the 227 KB limit");
 
 struct Args {
   void *out;
@@ -370,11 +379,11 @@ __device__ __forceinline__ void exponentials(const float (&s)[kKeys], float c, f
   }
 }
 // ------------------------------------------------------------------ the kernel
-template <bool kBF, int QA, int VA>
+template <bool kBF, int QA, int VA, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const Args a) {
-  using C = Cfg<QA, VA>;
+  using C = Cfg<QA, VA, kFew>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bar);
@@ -398,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::slots; ++s) { tc::mbar_init(kv_full + s, 1); tc::mbar_init(kv_empty + s, 2); }
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(s_full + t, 1);
-      tc::mbar_init(s_free + t, 4);
-      tc::mbar_init(p_full + 2 * t, 4);
-      tc::mbar_init(p_full + 2 * t + 1, 4);
+      tc::mbar_init(s_free + t, C::warps);
+      tc::mbar_init(p_full + 2 * t, C::warps);
+      tc::mbar_init(p_full + 2 * t + 1, C::warps);
       tc::mbar_init(pv_done + t, 1);
-      tc::mbar_init(o_free + t, 4);
+      tc::mbar_init(o_free + t, C::warps);
     }
-    for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 11); }
+    for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 3 + 2 * C::warps); }
     tc::mbar_init(done, 2);
     tc::mbar_init(block_full, 1);
     tc::fence_barrier_init();
@@ -510,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (it.u[t].nblk > 0)
 #pragma unroll
                 for (int c = 0; c < QA; ++c)
-                  tc::tma_load_4d(smem + C::q + ((qb * 2 + t) * QA + c) * kAtom, &tq, q_full + qb, 64 * c, 0, it.u[t].kvh,
-                                  it.u[t].q_row);
+                  tc::tma_load_4d(smem + C::q + qb * C::qbuf + (kFew ? 2 * c + t : t * QA + c) * C::tile, &tq, q_full + qb, 64 * c, 0,
+                                  it.u[t].kvh, it.u[t].q_row);
           }
           // element e of unit t's stream into the next slot
           auto fill = [&](int t, int e, int nb) {
@@ -555,10 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
       int ring = 0, qn = 0;             // next ring slot, q buffer
       uint32_t ring_phase = 0, q_phase = 0, units = 0, blocks = 0;  // parities: of those, and of this unit's
-      const uint64_t p_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::p) + t * kAtom);
+      const uint64_t p_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::p) + (kFew ? 0 : t * C::tile));
       // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
       // / 16, below 2^14 within shared memory)
-      const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * QA * kAtom);
+      const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::q) + t * C::unit);
       const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::kv)), v_desc0 = v_desc(tc::smem_u32(smem + C::kv));
       bool ok = true;
       for (int n = 0; ok && next_item(n, it); ++n) {
@@ -602,11 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](int j, int sl) {
           tc::tc_fence_after();
           const uint32_t id = klen - j * kKeys > kHalf ? id_s : id_s64;
-          const uint64_t qd = q_desc + ((qn * 2 * QA * kAtom) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
+          const uint64_t qd = q_desc + ((qn * C::qbuf) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4 * QA; ++kk)
             if (kk < qk_steps)
-              mma_ss(leader, tS, qd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
+              mma_ss(leader, tS, qd + (((kk / 4) * C::step + (kk % 4) * 32) >> 4),
                      kd + (((kk / 4) * kAtom + (kk % 4) * 32) >> 4), id, kk != 0);
           commit(leader, s_full + t);
           commit(leader, kv_empty + sl);
@@ -677,16 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    // ---------------- softmax and output of unit t: row r of the tile
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    // ---------------- softmax and output of unit t: row r of the tile, in tensor memory's lanes from `first` on
+    const int t = warp >> 2, first = 32 * (warp & 3), r = kFew ? lane : first + lane;
     const int tok = r / a.G, head = r - tok * a.G;
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t lane_off = (uint32_t)first << 16;
     const uint32_t tS = tmem + 128 * t + lane_off, tO = tmem + kOCol + kOStep * t + lane_off;
     const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t + lane_off;
     const float c = a.scale_log2;
     uint32_t blocks = 0;  // of this unit in all
     Item it;
-    for (int n = 0; next_item(n, it); ++n) {
+    for (int n = 0; (!kFew || (warp & 3) == t) && next_item(n, it); ++n) {
       const int nb = it.u[t].nblk;
       const bool row = tok < it.u[t].ntok && r < a.TQ * a.G;
       const bool live = __any_sync(0xffffffffu, row);  // a warp without rows only keeps the barriers going
@@ -758,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         exponentials<kBF, kHalf + kLate, kKeys>(sv, c, negm, sum, pk1 + kLate / 2);
         if (C::overlay) {
           if (!previous_pv()) { ok = false; break; }
-          uint8_t *pr = smem + C::p + t * kAtom + r * 128;  // 128-byte rows of 64 keys, 16-byte chunk i of row r at i ^ (r % 8)
+          uint8_t *pr = smem + C::p + ((kFew ? 0 : t * kRows) + first + lane) * 128;  // 128-byte rows of 64 keys, 16-byte chunk i of row r at i ^ (r % 8)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<uint4 *>(pr + ((k ^ (r & 7)) << 4)) = make_uint4(pk1[4 * k], pk1[4 * k + 1], pk1[4 * k + 2], pk1[4 * k + 3]);
@@ -903,10 +912,10 @@ int current_device() {
   return dev;
 }
 
-template <bool kBF, int QA, int VA>
+template <bool kBF, int QA, int VA, bool kFew>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
-  auto *k = attn_packed_kernel<kBF, QA, VA>;
-  const int smem = Cfg<QA, VA>::total + 1024;
+  auto *k = attn_packed_kernel<kBF, QA, VA, kFew>;
+  const int smem = Cfg<QA, VA, kFew>::total + 1024;
   static std::atomic<unsigned long long> ready{0};  // devices whose limits are set
   const int dev = current_device();
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
@@ -934,22 +943,26 @@ int sm_count() {
   return n;
 }
 
+// Sequences whose queries fill no more than 32 rows of a tile on average (single new tokens) take tiles of 32.
+bool few_rows(const mrf_attention_args &a) { return a.q_rows * (a.heads / a.kv_heads) <= 32ll * a.seqs && a.heads / a.kv_heads <= 32; }
+int tile_tokens(const mrf_attention_args &a) { return (few_rows(a) ? 32 : kRows) / (a.heads / a.kv_heads); }
+
 // How keys are split when there are few tiles: the keys of a range (0: no splits) and the most ranges a
 // sequence can have.
 struct Split {
   int chunk, most;
 };
 Split split_of(const mrf_attention_args &a) {
-  const int G = a.heads / a.kv_heads, TQ = kRows / G;
+  const int TQ = tile_tokens(a);
   const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ), units = tiles * a.kv_heads, sms = sm_count();
   const long long keys = a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows, blocks = (keys + kKeys - 1) / kKeys;
   // More units than SMs: only single tiles (new tokens) of sequences whose lengths only the device knows,
   // where a long one would keep its SM while the others are done.
   if (blocks < 8 || units > (tiles > a.seqs || a.seqs == 1 ? sms : 4 * sms)) return {0, 1};
   // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
-  // about four rounds if all were as long as the longest; from 512 keys on a range's own cost (its
+  // about eight rounds if all were as long as the longest; from 512 keys on a range's own cost (its
   // queries, its output in fp32) is small.
-  const long long wanted = a.seqs == 1 ? 2 * (sms / units) : std::max(1ll, 8 * sms / units);
+  const long long wanted = a.seqs == 1 ? 2 * (sms / units) : std::max(1ll, 16 * sms / units);
   long long chunk = (blocks + std::max(1ll, wanted) - 1) / std::max(1ll, wanted);
   chunk = std::max(chunk, a.seqs == 1 ? 2ll : 4ll);
   chunk = std::max(chunk, (blocks + 127) / 128);
@@ -995,7 +1008,7 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   a.heads = m.heads;
   a.kv_heads = m.kv_heads;
   a.G = m.heads / m.kv_heads;
-  a.TQ = kRows / a.G;
+  a.TQ = tile_tokens(m);
   a.width = m.width;
   a.v_width = m.v_width;
   a.causal = m.causal != 0;
@@ -1027,11 +1040,11 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   const long long items = a.chunk ? tiles * m.kv_heads * ((a.max_splits + 1) / 2)
                                   : tiles / 2 * m.kv_heads + std::min<long long>(m.seqs, tiles) * ((m.kv_heads + 1) / 2);
   const int grid = (int)std::max(1ll, items);
-  const bool bf = m.dtype == MRF_DTYPE_BF16, q2 = m.width > 64, v2 = m.v_width > 64;
-#define MRF_ATTN(BF)                                                                                         \
-  (q2 ? (v2 ? launch<BF, 2, 2>(tq, tk, tv, a, grid, st) : launch<BF, 2, 1>(tq, tk, tv, a, grid, st))         \
-      : (v2 ? launch<BF, 1, 2>(tq, tk, tv, a, grid, st) : launch<BF, 1, 1>(tq, tk, tv, a, grid, st)))
-  *err = bf ? MRF_ATTN(true) : MRF_ATTN(false);
+  const bool bf = m.dtype == MRF_DTYPE_BF16, few = few_rows(m), q2 = m.width > 64, v2 = m.v_width > 64;
+#define MRF_ATTN(BF, FEW)                                                                                        \
+  (q2 ? (v2 ? launch<BF, 2, 2, FEW>(tq, tk, tv, a, grid, st) : launch<BF, 2, 1, FEW>(tq, tk, tv, a, grid, st))   \
+      : (v2 ? launch<BF, 1, 2, FEW>(tq, tk, tv, a, grid, st) : launch<BF, 1, 1, FEW>(tq, tk, tv, a, grid, st)))
+  *err = bf ? (few ? MRF_ATTN(true, true) : MRF_ATTN(true, false)) : (few ? MRF_ATTN(false, true) : MRF_ATTN(false, false));
 #undef MRF_ATTN
   if (*err != cudaSuccess || a.chunk == 0) return true;
   cudaLaunchConfig_t cfg = {};
