@@ -271,15 +271,17 @@ def _code(t, x, name, dev=None):
     return code
 
 
-def _like(x, dtype, dev, shape, name):
+def _like(t, x, dtype, dev, shape, name):
     """`x` is a tensor of the given type, device and shape, its last dimension contiguous; its strides."""
-    if x.dtype != dtype or x.get_device() != dev:
-        raise MrfError(-1, f"{name} must be {dtype} on cuda:{dev}, is {x.dtype} on {x.device}")
+    if not isinstance(x, t.Tensor) or x.dtype != dtype or x.get_device() != dev:
+        raise MrfError(-1, f"{name} must be {dtype} on cuda:{dev}, is {getattr(x, 'dtype', type(x))} on {getattr(x, 'device', None)}")
     if x.shape != shape:
         raise MrfError(-2, f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
     st = x.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise MrfError(-1, f"{name}: the last dimension must be contiguous")
+    if x.requires_grad and t.grad():
+        raise MrfError(-1, f"{name} requires a gradient; the library is for inference")
     return st
 
 
@@ -342,49 +344,54 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, out_dtype=None, group=0, c
     `group` columns (0: the row), out * scale standing for the value.  out=x norms in place,
     residual_out=residual updates the residual in place; without residual_out h gets a new tensor.
     Returns RmsNorm(out, scales, residual)."""
-    t = _t()
+    t = _torch or _t()
     code = _code(t, x, "x")
     dev = x.get_device()
     if stream is not None or dev != t.device():
         with _scope(dev, stream):
             return rms_norm(x, weight, eps, residual, out_dtype, group, clamp, out, residual_out)
-    shape = x.shape
+    shape, dtype = x.shape, x.dtype
     if len(shape) == 0 or shape[-1] < 1:
         raise MrfError(-2, "x must have a last dimension of at least 1")
-    dim, dtype = shape[-1], x.dtype
-    quant = out_dtype == t.e4m3
+    dim = shape[-1]
+    quant = out_dtype is t.e4m3
     if not quant and out_dtype is not None and out_dtype != dtype:
         raise MrfError(-1, f"out_dtype must be {dtype} or torch.float8_e4m3fn, got {out_dtype}")
-    x_row = _row_stride(x, _like(x, dtype, dev, shape, "x"), dim, "x")
+    whole = x.is_contiguous()
+    x_row = dim if whole else _row_stride(x, _like(t, x, dtype, dev, shape, "x"), dim, "x")
     w = wcode = res = res_row = res_out = res_out_row = scale_ptr = 0
     if weight is not None:
         wcode = _code(t, weight, "weight", dev)
-        if weight.shape != (dim,) or (dim > 1 and weight.stride(0) != 1):
+        if weight.shape != (dim,) or not weight.is_contiguous():
             raise MrfError(-2, f"weight must be a contiguous vector of {dim} values, got {tuple(weight.shape)}")
         w = weight.data_ptr()
     h, scales = residual_out, None
     if residual is not None:
-        _code(t, residual, "residual", dev)
-        res_row = _row_stride(residual, _like(residual, dtype, dev, shape, "residual"), dim, "residual")
+        res_row = _row_stride(residual, _like(t, residual, dtype, dev, shape, "residual"), dim, "residual")
         res = residual.data_ptr()
         if h is None:
-            h, res_out_row = t.empty_like(x) if x.is_contiguous() else x.new_empty(shape), dim
+            h, res_out_row = t.empty_like(x) if whole else x.new_empty(shape), dim
         else:
-            res_out_row = _row_stride(h, _like(h, dtype, dev, shape, "residual_out"), dim, "residual_out")
+            res_out_row = _row_stride(h, _like(t, h, dtype, dev, shape, "residual_out"), dim, "residual_out")
         res_out = h.data_ptr()
     elif h is not None:
         raise MrfError(-1, "residual_out without residual")
-    if out is None:
-        kind = t.e4m3 if quant else dtype
-        out, out_row = t.empty_like(x, dtype=kind) if x.is_contiguous() else x.new_empty(shape, dtype=kind), dim
-    else:
-        out_row = _row_stride(out, _like(out, t.e4m3 if quant else dtype, dev, shape, "out"), dim, "out")
     if quant:
+        if out is None:
+            out, out_row = t.empty_like(x, dtype=t.e4m3) if whole else x.new_empty(shape, dtype=t.e4m3), dim
+        else:
+            out_row = _row_stride(out, _like(t, out, t.e4m3, dev, shape, "out"), dim, "out")
         scales = x.new_empty(shape[:-1] + (-(-dim // group) if group > 0 else 1,), dtype=t.f32)
         scale_ptr = scales.data_ptr()
-    _check(lib().mrf_rms_norm(_NORM.pack(
+    elif out is None:
+        out, out_row = t.empty_like(x) if whole else x.new_empty(shape), dim
+    else:
+        out_row = _row_stride(out, _like(t, out, dtype, dev, shape, "out"), dim, "out")
+    status = (_lib or lib()).mrf_rms_norm(_NORM.pack(
         x.data_ptr(), res, w, out.data_ptr(), res_out, scale_ptr, x.numel() // dim, x_row, res_row, out_row, res_out_row,
-        dim, code, wcode, 3 if quant else code, group, bool(clamp), eps), t.stream(dev)))
+        dim, code, wcode, 3 if quant else code, group, bool(clamp), eps), t.stream(dev))
+    if status:
+        _check(status)
     return RmsNorm(out, scales, h)
 
 
@@ -416,7 +423,7 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     [tokens, kv_heads, width] (or None) turned by each token's position (int32 or int64 [tokens]), in pairs
     (2i, 2i + 1), or (i, i + part / 2) with interleaved=False.  Heads and tokens may have any strides
     (column ranges of a projection's rows); q_out=q and k_out=k turn in place.  Returns (q_out, k_out)."""
-    t = _t()
+    t = _torch or _t()
     code = _code(t, q, "q")
     dev = q.get_device()
     if stream is not None or dev != t.device():
@@ -426,20 +433,20 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     if len(shape) != 3:
         raise MrfError(-2, f"q must be [tokens, heads, width], got {tuple(shape)}")
     tokens, heads, width = shape
-    qs = _like(q, dtype, dev, shape, "q")
+    qs = _like(t, q, dtype, dev, shape, "q")
     ks = kos = (0, 0, 1)
     kv_heads = k_ptr = k_out_ptr = 0
     if k is not None:
-        _code(t, k, "k", dev)
         if k.dim() != 3:
             raise MrfError(-2, f"k must be [tokens, kv_heads, width], got {tuple(k.shape)}")
         kv_heads = k.shape[1]
-        ks = _like(k, dtype, dev, (tokens, kv_heads, width), "k")
+        k_shape = (tokens, kv_heads, width)
+        ks = _like(t, k, dtype, dev, k_shape, "k")
         if k_out is None:
             k_out = t.empty_like(k)
             kos = k_out.stride()
         else:
-            kos = _like(k_out, dtype, dev, (tokens, kv_heads, width), "k_out")
+            kos = _like(t, k_out, dtype, dev, k_shape, "k_out")
         k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise MrfError(-1, "k_out without k")
@@ -450,11 +457,13 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
         q_out = t.empty_like(q)
         qos = q_out.stride()
     else:
-        qos = _like(q_out, dtype, dev, shape, "q_out")
-    _check(lib().mrf_rope(_ROPE.pack(
+        qos = _like(t, q_out, dtype, dev, shape, "q_out")
+    status = (_lib or lib()).mrf_rope(_ROPE.pack(
         q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(), table.turns.data_ptr(), tokens, qs[0], qs[1],
-        ks[0], ks[1], qos[0], qos[1], kos[0], kos[1], heads, kv_heads, width, table.part, code, positions.dtype == t.i64,
-        bool(interleaved), table.scale), t.stream(dev)))
+        ks[0], ks[1], qos[0], qos[1], kos[0], kos[1], heads, kv_heads, width, table.part, code, positions.dtype is t.i64,
+        bool(interleaved), table.scale), t.stream(dev))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
@@ -469,54 +478,55 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
     bound of the key counts known on the host (0: k's rows), which only decides how the work is split.
     Rows of no sequence keep what `out` held (a new `out` is uninitialised there).  Returns out
     [q_rows, heads, v_width], or (out, lse float32 [q_rows, heads]) with return_lse."""
-    t = _t()
+    t = _torch or _t()
     code = _code(t, q, "q")
     dev = q.get_device()
     if stream is not None or dev != t.device():
         with _scope(dev, stream):
             return attention_packed(q, k, v, q_offsets, k_start, k_len, max_k, causal, scale, out, return_lse)
-    _code(t, k, "k", dev)
-    _code(t, v, "v", dev)
     dtype, shape, v_shape = q.dtype, q.shape, v.shape
     if len(shape) != 3 or len(v_shape) != 3:
         raise MrfError(-2, f"q and v must be [rows, heads, width], got {tuple(shape)} and {tuple(v_shape)}")
     q_rows, heads, width = shape
     k_rows, kv_heads, v_width = v_shape
-    qs, ks, vs = (_like(q, dtype, dev, shape, "q"), _like(k, dtype, dev, (k_rows, kv_heads, width), "k"),
-                  _like(v, dtype, dev, v_shape, "v"))
+    q_st, q_sh, _ = _like(t, q, dtype, dev, shape, "q")
+    k_st, k_sh, _ = _like(t, k, dtype, dev, (k_rows, kv_heads, width), "k")
+    v_st, v_sh, _ = _like(t, v, dtype, dev, v_shape, "v")
     if not isinstance(q_offsets, t.Tensor) or q_offsets.dim() != 1 or q_offsets.shape[0] < 1:
         raise MrfError(-2, "q_offsets must be a vector of seqs + 1 values")
     seqs = q_offsets.shape[0] - 1
     _vector(t, q_offsets, dev, seqs + 1, "q_offsets")
-    if (k_start is None) != (k_len is None):
-        raise MrfError(-1, "k_start and k_len go together")
-    start_ptr = len_ptr = lse_ptr = 0
-    if k_len is not None:
+    start_ptr = len_ptr = lse_ptr = space_ptr = 0
+    if k_len is not None and k_start is not None:
         _vector(t, k_start, dev, seqs, "k_start")
         _vector(t, k_len, dev, seqs, "k_len")
         # (a vector of no values has a null pointer; any other says that k_start and k_len are given)
         start_ptr, len_ptr = (k_start.data_ptr(), k_len.data_ptr()) if seqs else (8, 8)
+    elif k_len is not None or k_start is not None:
+        raise MrfError(-1, "k_start and k_len go together")
     if out is None:
         out = t.empty_like(q) if v_width == width else q.new_empty((q_rows, heads, v_width))
-        os_ = out.stride()
+        o_st, o_sh, _ = out.stride()
     else:
-        os_ = _like(out, dtype, dev, (q_rows, heads, v_width), "out")
+        o_st, o_sh, _ = _like(t, out, dtype, dev, (q_rows, heads, v_width), "out")
     lse = None
     if return_lse:
         lse = q.new_empty((q_rows, heads), dtype=t.f32)
         lse_ptr = lse.data_ptr()
-    L = lib()
-    args = [q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, q_offsets.data_ptr(), start_ptr, len_ptr, 0, 0,
-            q_rows, k_rows, max_k, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], seqs, heads, kv_heads, width, v_width,
-            code, bool(causal), width ** -0.5 if scale is None else scale]
-    packed = _ATTENTION.pack(*args)
-    need = ctypes.c_size_t()
-    _check(L.mrf_attention_workspace(packed, ctypes.byref(need)))
+    L, need = _lib or lib(), ctypes.c_size_t()
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, q_offsets.data_ptr(), start_ptr, len_ptr)
+    tail = (q_rows, k_rows, max_k, q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh, seqs, heads, kv_heads, width, v_width, code,
+            bool(causal), width ** -0.5 if scale is None else scale)
+    packed = _ATTENTION.pack(*head, 0, 0, *tail)
+    status = L.mrf_attention_workspace(packed, ctypes.byref(need))
+    if status:
+        _check(status)
     if need.value:
         space = q.new_empty(need.value, dtype=t.u8)
-        args[8], args[9] = space.data_ptr(), need.value
-        packed = _ATTENTION.pack(*args)
-    _check(L.mrf_attention(packed, t.stream(dev)))
+        packed = _ATTENTION.pack(*head, space.data_ptr(), need.value, *tail)
+    status = L.mrf_attention(packed, t.stream(dev))
+    if status:
+        _check(status)
     return (out, lse) if return_lse else out
 
 
