@@ -55,8 +55,8 @@ constexpr int kRows = 128, kKeys = 128, kHalf = 64;
 constexpr int kLate = 32;           // keys of P's second half whose exponentials run before the first half is handed over
 constexpr int kAtom = kRows * 128;  // 64 16-bit values of 128 rows
 constexpr int kThreads = 384;
-// register split, as in the model's attention: 2 * 128 * 200 + 128 * 96 <= 384 * 168
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsIo = 96;
+// register split, as in the model's attention: 2 * 128 * 208 + 128 * 72 <= 384 * 168
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
 constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
 constexpr int kItems = 1;            // ring of work items: the next one is taken when everybody has begun this one
@@ -182,9 +182,9 @@ __device__ __forceinline__ void tmem_landed(uint32_t *r) {
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 // 8 columns of this thread's lane times f (few registers: scores are held while it runs)
@@ -368,13 +368,13 @@ __device__ __forceinline__ float row_max(const float (&s)[kKeys]) {
 
 // pk <- 2^(c s + negm) of the keys kA .. kB, two 16-bit values each, and their unrounded sums
 template <bool kBF, int kA, int kB>
-__device__ __forceinline__ void exponentials(const float (&s)[kKeys], float c, float negm, float2 (&sum)[4], uint32_t *pk) {
+__device__ __forceinline__ void exponentials(const float (&s)[kKeys], float c, float negm, float2 (&sum)[2], uint32_t *pk) {
   const float2 c2 = make_float2(c, c), n2 = make_float2(negm, negm);
 #pragma unroll
   for (int k = kA; k < kB; k += 2) {
     const float2 d = __ffma2_rn(make_float2(s[k], s[k + 1]), c2, n2);
     const float2 p = make_float2(ex2(d.x), ex2(d.y));
-    sum[k / 2 % 4] = __fadd2_rn(sum[k / 2 % 4], p);
+    sum[k / 2 % 2] = __fadd2_rn(sum[k / 2 % 2], p);
     pk[(k - kA) / 2] = pack2<kBF>(p.x, p.y);
   }
 }
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool any_need = __any_sync(0xffffffffu, need);
         // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
         const float negm = m == -INFINITY ? 0.f : -m * c;
-        float2 sum[4] = {};
+        float2 sum[2] = {};
         uint32_t pk[kHalf / 2];
         exponentials<kBF, 0, kHalf>(sv, c, negm, sum, pk);
         // What P and O were used for before: with narrow v the previous block's P V read all of P_t; with
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((!C::overlay || any_need) && !previous_pv()) { ok = false; break; }
         tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + k, pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
+        for (int k = 0; k < kHalf / 2; k += 8) tmem_st8(tP + k, pk + k);
         if (any_need) {  // O_t moves to the new maximum
 #pragma unroll
           for (int k = 0; k < 64 * VA; k += 8) tmem_scale8(tO + k, alpha);
@@ -774,14 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_proxy_async();
         } else {
 #pragma unroll
-          for (int k = 0; k < kHalf / 2; k += 4) tmem_st4(tP + kHalf / 2 + k, pk1[k], pk1[k + 1], pk1[k + 2], pk1[k + 3]);
+          for (int k = 0; k < kHalf / 2; k += 8) tmem_st8(tP + kHalf / 2 + k, pk1 + k);
           tmem_wait_st();
           tc::tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + 2 * t + 1);
-        const float2 s4 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-        l += s4.x + s4.y;
+        const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+        l += s2.x + s2.y;
       }
       if (!ok) break;
       if (nb > 0) {
