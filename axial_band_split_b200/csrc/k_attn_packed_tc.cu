@@ -92,7 +92,7 @@ struct Cfg {
   static constexpr int qbuf = 2 * QA * tile;
   static constexpr int slot = (QA > VA ? QA : VA) * kAtom;
   static constexpr int q = 0;
-  static constexpr int p = q + qbufs * qbuf;         // the second half of P
+  static constexpr int p = q + qbufs * qbuf;         // the second half of P; the output's way out
   static constexpr int kv = p + (overlay ? 2 * tile : 0);
   static constexpr int slots = (14 * kAtom - kv) / slot;  // ring of K or V blocks
   static constexpr int bar = kv + slots * slot;
@@ -790,28 +790,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that saw no key: zeros
       const long long at = (long long)it.u[t].q_row + tok;
-      const int h = it.u[t].kvh * a.G + head;
-#pragma unroll
+      const int h = it.u[t].kvh * a.G + head, size = it.partial ? 4 : 2;
+      // With whole tiles and wide v the output goes by 128 bytes of each row through this warp's rows of the P area (the
+      // last P V has read it), so that a store instruction writes whole pieces of 4 rows: 16 bytes of 32 rows
+      // at a time took 9000 clk a tile of 128 columns.  Otherwise rows are stored as they are.
+      constexpr bool kStage = VA == 2 && !kFew;
+      unsigned long long mine = 0;
+      if (row)
+        mine = it.partial ? reinterpret_cast<unsigned long long>(a.part + (((long long)it.u[t].split * a.q_rows + at) * a.heads + h) * a.v_width)
+                          : reinterpret_cast<unsigned long long>(static_cast<uint16_t *>(a.out) + at * a.out_token_stride + h * a.out_head_stride);
+      uint8_t *stage = smem + C::p + (t * kRows + first) * 128;
+#pragma unroll 1
       for (int i = 0; i < 64 * VA; i += 32) {
         if (!live || i >= a.v_width) break;
         float v[32];
         if (nb > 0) tc::tmem_ld32(tO + i, v);
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = inv == 0.f ? 0.f : v[k] * inv;
-        if (row && it.partial) {
-          float *o = a.part + (((long long)it.u[t].split * a.q_rows + at) * a.heads + h) * a.v_width + i;
+        // chunk: 16 bytes of the row from this pass's first
+        auto put = [&](int chunk, uint4 u) {
+          if constexpr (!kStage) {
+            const int byte = i * size + chunk * 16;
+            if (mine != 0 && byte < a.v_width * size) *reinterpret_cast<uint4 *>(mine + byte) = u;
+          } else {
+            const int c = it.partial ? chunk : (i & 32) / 8 + chunk;
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = u;
+          }
+        };
+        if (it.partial) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
-            if (i + k < a.v_width) *reinterpret_cast<float4 *>(o + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        } else if (row) {
-          uint16_t *o = static_cast<uint16_t *>(a.out) + at * a.out_token_stride + h * a.out_head_stride + i;
+            put(k / 4, make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])));
+        } else {
 #pragma unroll
           for (int k = 0; k < 32; k += 8)
-            if (i + k < a.v_width)
-              *reinterpret_cast<uint4 *>(o + k) = make_uint4(pack2<kBF>(v[k], v[k + 1]), pack2<kBF>(v[k + 2], v[k + 3]),
-                                                             pack2<kBF>(v[k + 4], v[k + 5]), pack2<kBF>(v[k + 6], v[k + 7]));
+            put(k / 8, make_uint4(pack2<kBF>(v[k], v[k + 1]), pack2<kBF>(v[k + 2], v[k + 3]), pack2<kBF>(v[k + 4], v[k + 5]),
+                                  pack2<kBF>(v[k + 6], v[k + 7])));
         }
         __syncwarp();
+        if (kStage && (it.partial || (i & 32) || i + 32 >= a.v_width)) {
+          const int byte = (it.partial ? i * 4 : (i & ~63) * 2) + (lane & 7) * 16;  // within the row
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int rr = r0 + (lane >> 3);
+            const unsigned long long to = __shfl_sync(0xffffffffu, mine, rr);
+            if (to != 0 && byte < a.v_width * size)
+              *reinterpret_cast<uint4 *>(to + byte) = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          }
+          __syncwarp();
+        }
       }
       if (nb > 0) {
         tc::tc_fence_before();

@@ -415,7 +415,8 @@ def rope_table(part, theta=10000.0, scaling="none", factor=1.0, original=0, beta
     turns = np.zeros(max(1, min(part, 1024) // 2), np.uint64)
     scale = ctypes.c_float(0)
     _check(lib().mrf_rope_table(ctypes.byref(c), turns.ctypes.data_as(ctypes.c_void_p), ctypes.byref(scale)))
-    return RopeTable(torch.from_numpy(turns.view(np.int64)).to(device), scale.value, part)
+    # (not waited for: the copy has left this memory when the call returns, and the stream orders its use)
+    return RopeTable(torch.from_numpy(turns.view(np.int64)).to(device, non_blocking=True), scale.value, part)
 
 
 def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, stream=None):
