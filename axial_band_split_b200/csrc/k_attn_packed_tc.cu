@@ -4,9 +4,9 @@
 // the SM.
 //
 // Tiles.  The G = heads / kv_heads query heads that share a key head are rows of one matrix: a tile
-// is TQ = 128 / G tokens (32 / G for single new tokens, see Cfg) x G heads (row = token * G + head, one bulk tensor load of a (64, G, 1, TQ)
-// box per 64 dimensions), so each key block is read once for all of them and a single new token
-// already fills G rows.  Key blocks are 128 rows.
+// is TQ = 128 / G tokens (32 / G for single new tokens, see Cfg) x G heads, row = token * G + head, one
+// bulk tensor load of a (64, G, 1, TQ) box per 64 dimensions.  So each key block is read once for all of
+// them and a single new token already fills G rows.  Key blocks are 128 rows.
 //
 // Work items.  A CTA runs two units (a tile with a range of keys) t = 0, 1 side by side:
 //   pair   - two neighbouring tiles of one sequence and key head: they share every key block;
@@ -16,9 +16,9 @@
 //            sequences, leave their own outputs and log-sums in the workspace, and combine_kernel joins them.
 // Items are numbered sequence by sequence, a causal sequence's last tiles (the most keys) first.  The grid
 // has a block for each; a running CTA takes over blocks that have not been launched (cluster launch
-// control), so that items go to whoever is free, in order.  Lengths live in device memory, so warp 11 finds each item's
-// sequence by a running prefix sum over the sequences' item counts and hands it to the others
-// through a ring in shared memory.
+// control), so that items go to whoever is free, in order.  Lengths live in device memory, so warp 11
+// finds each item's sequence by a running prefix sum over the sequences' item counts and hands it to the
+// others through shared memory.
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, one score row per thread; warp 8: bulk tensor loads;
 // warps 9, 10: matrix instructions of unit 0, 1; warp 11: items.
@@ -253,6 +253,17 @@ __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
   }
 }
 
+// Waits for work items last as long as items do: up to a minute, ended by the abort flag that any other
+// expired wait (within seconds) raises.
+__device__ __forceinline__ bool wait_item(uint64_t *bar, uint32_t parity, unsigned *status, unsigned site, volatile int *abort) {
+  const unsigned long long t0 = tc::globaltimer();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (tc::globaltimer() - t0 > 60000000000ull) return tc::mbar_wait(bar, parity, status, site, abort);
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ sequences and items
 struct Seq {
   int q0, nq, k0, nk;
@@ -424,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   tc::griddep_wait();
-  tc::griddep_launch_dependents();
+  if (a.chunk) tc::griddep_launch_dependents();  // combine_kernel
   constexpr uint32_t kOCol = 256, kOStep = 64 * VA;
 
   // the n-th item, copied from the ring; false when there is none left or a wait expired
   auto next_item = [&](int n, Item &it) {
-    if (!tc::mbar_wait(item_full + n % kItems, (n / kItems) & 1, status, 50, abort)) return false;
+    if (!wait_item(item_full + n % kItems, (n / kItems) & 1, status, 50, abort)) return false;
     it = items[n % kItems];
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(item_empty + n % kItems);
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load();
       long long it = blockIdx.x;
       for (int n = 0, asked = 0;; ++n) {
-        if (!tc::mbar_wait(item_empty + n % kItems, ((n / kItems) & 1) ^ 1, status, 51, abort)) break;
+        if (!wait_item(item_empty + n % kItems, ((n / kItems) & 1) ^ 1, status, 51, abort)) break;
         Item item;
         item.last = 1;
         // the next block that has an item (the grid may have more blocks than there are items: those are

@@ -468,7 +468,7 @@ cudaError_t launch(const mrf_rms_norm_args &a, cudaStream_t st) {
   Plan p;
   p.wide = a.weight_dtype == MRF_DTYPE_F32 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
   p.inv_dim = 1.f / (float)a.dim;
-  p.inv_eps = 1.f / a.eps;
+  p.inv_eps = std::min(1.f / a.eps, 3.4e38f);  // finite: a row of zeros stays zeros
   p.log2_group = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   const int chunks = (a.dim + 255) / 256;  // of 256 columns: a vector of each lane of a warp
   const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs: more threads a row, shorter chains

@@ -61,7 +61,7 @@ def test_norm_refusals(change, status):
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dtype=3), EINVAL), (dict(tokens=-1), ESHAPE), (dict(heads=0), ESHAPE), (dict(kv_heads=-1), ESHAPE),
+    (dict(dtype=3), EINVAL), (dict(tokens=-1), ESHAPE), (dict(tokens=1 << 31), ESHAPE), (dict(heads=0), ESHAPE), (dict(kv_heads=-1), ESHAPE),
     (dict(k=None), ESHAPE), (dict(width=1, part=2), ESHAPE), (dict(width=1026), ESHAPE), (dict(part=0), ESHAPE),
     (dict(part=66), ESHAPE), (dict(part=33), ESHAPE), (dict(scale=math.nan), EINVAL), (dict(q=None), EINVAL),
     (dict(q_out=None), EINVAL), (dict(k_out=None), EINVAL), (dict(positions=None), EINVAL), (dict(turns=None), EINVAL),

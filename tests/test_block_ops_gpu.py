@@ -306,6 +306,37 @@ def test_attention_cold_inputs_give_the_same_bits():
             assert all(torch.equal(o[:n], outs[-1][:n]) for o in outs[:-1])
 
 
+def test_attention_many_sequences():
+    """More sequences than the 32 that are looked at together, empty ones among them, and a key bound that is too low."""
+    run(Shape([(n % 5, None) for n in range(333)], 4, 2))
+    run(Shape([(n % 3, 7 * n % 400) for n in range(150)], 8, 2, 128, 128, F16, causal=False))
+    run(Shape([(1, 13 * n % 3000) for n in range(70)], 4, 4, 64, 64, BF16, max_k=3000))
+    run(Shape([(0, 5)] * 40 + [(130, 2000)] + [(0, 0)] * 40 + [(1, 4097)], 2, 1, 128, 128, max_k=4097))
+    run(Shape([(1, 6000), (1, 100), (2, 1025)], 8, 1, 128, 128, max_k=1024))
+    run(Shape([(1, 6000)], 8, 1, 64, 64, max_k=1024))
+
+
+def test_attention_from_two_threads():
+    """Calls of two threads on their own streams do not disturb one another."""
+    import threading
+    cases = [make(Shape([(1, 9000 + 77 * i), (1, 50)], 8, 1, 128, 128), 40 + i) for i in range(2)]
+    want = [mrf.attention_packed(*c[:6], 9100) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for _ in range(30):
+            got = mrf.attention_packed(*cases[i][:6], 9100, stream=stream)
+            stream.synchronize()
+            bad.append(not torch.equal(got[:2], want[i][:2]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(bad) == 60 and not any(bad)
+
+
 def test_attention_large_scores_and_peaks():
     """Scores of hundreds (running maxima that jump between key blocks) and one key that takes all the weight."""
     for width in (64, 128):
