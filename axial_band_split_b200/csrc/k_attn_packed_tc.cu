@@ -994,20 +994,23 @@ Split split_of(const mrf_attention_args &a) {
   const int TQ = tile_tokens(a);
   const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ), units = tiles * a.kv_heads, sms = sm_count();
   const long long keys = a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows, blocks = (keys + kKeys - 1) / kKeys;
-  // More units than SMs: only single tiles (new tokens) of sequences whose lengths only the device knows,
-  // where a long one would keep its SM while the others are done.
-  if (blocks < 8 || units > (tiles > a.seqs || a.seqs == 1 ? sms : 4 * sms)) return {0, 1};
+  // More units than SMs: only single tiles (new tokens) of long sequences whose lengths only the device knows,
+  // where the longest would keep its SM while the others are done (32 sequences up to 8192 keys, 8 key
+  // heads: 110 us against 142; up to 1024: 34 against 26).
+  if (blocks < 8 || units > (tiles > a.seqs || a.seqs == 1 || blocks < 32 ? sms : 4 * sms)) return {0, 1};
   // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
-  // about eight rounds if all were as long as the longest; from 512 keys on a range's own cost (its
-  // queries, its output in fp32) is small.
-  const long long wanted = a.seqs == 1 ? 2 * (sms / units) : std::max(1ll, 16 * sms / units);
-  long long chunk = (blocks + std::max(1ll, wanted) - 1) / std::max(1ll, wanted);
-  chunk = std::max(chunk, a.seqs == 1 ? 2ll : 4ll);
-  chunk = std::max(chunk, (blocks + 127) / 128);
+  // about eight rounds if all were as long as the longest.
+  long long wanted = a.seqs == 1 ? 2 * (sms / units) : 16 * sms / units;
+  // A range's output is written and read again in fp32, at about 5 TB/s, against about 2 us a key block:
+  // the number of ranges where their sum is least.
+  const double bytes = (double)a.q_rows * a.heads * a.v_width * 8;
+  wanted = std::min<long long>(wanted, (long long)std::sqrt(blocks * 2.0 / (bytes / 5e6)));
+  if (wanted < 2) return {0, 1};
+  long long chunk = (blocks + wanted - 1) / wanted;
+  // (several sequences, 4 up to 8192 keys: at least 1, 2, 3, 4 blocks a range 36, 32, 31, 34 us)
+  chunk = std::max<long long>({chunk, a.seqs == 1 ? 1 : 3, (blocks + 127) / 128});
   const long long most = (blocks + chunk - 1) / chunk;
-  // what the ranges write and read again in fp32 stays below half of the keys and values they read
-  if (most < 2 || most * a.q_rows * a.heads * a.v_width * 8 > units * keys * (a.width + a.v_width)) return {0, 1};
-  return {(int)(chunk * kKeys), (int)most};
+  return most < 2 ? Split{0, 1} : Split{(int)(chunk * kKeys), (int)most};
 }
 
 bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
