@@ -6,10 +6,13 @@
 // row's sum of squares and the maxima that the 8-bit scales need come from the same pass over the
 // registers, and one exchange between the warps serves both.
 //
-// Rows up to 512 wide take a warp each (no exchange between warps), wider ones a block; a thread
-// holds V vectors of 8 values.  The arithmetic, about 10 instructions a value with the conversions,
-// is the next bound: it runs on packed fp32 pairs, and the work that a row costs every thread (the
-// sums' exchange, the root, the scales) is spread over the thread's 16 values.
+// Rows up to 256 wide take a warp each (no exchange between warps), wider ones a block.  Rows in 16-byte pieces
+// stream through rms_norm_stream_kernel, few, narrow or very wide ones go through rms_norm_kernel, and rows without
+// that alignment through rms_norm_odd_kernel.  The arithmetic, about 10 instructions a value with the conversions,
+// is the next bound: it runs on packed fp32 pairs, and the work that a row costs every thread (the sums' exchange,
+// the root, the scales) is spread over its 16 values.
+// 16384 x 4096 bf16 with residual and an e4m3 output (472 MB): 87.5 us, 5.4 TB/s, 0.82 of the measured copy
+// (a first form with 64-bit index products and a division a value executed 40 instructions a value: 113 us).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -27,14 +30,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // keeps a NaN
 __device__ __forceinline__ float warp_max(float v, int width) {
   for (int o = width / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
-}
-
-// 8 values of a row as they lie in memory.
-// Columns of value e of this lane's vector, whose warp's 256 columns begin at c0.  kVec: 8 neighbours
-// (16-byte accesses); else 32 apart, so that a warp's accesses of one value are neighbours.
-template <bool kVec>
-__device__ __forceinline__ int column(int c0, int lane, int e) {
-  return kVec ? c0 + 8 * lane + e : c0 + 32 * e + lane;
 }
 
 // Two 16-bit values as fp32, and back.
@@ -61,27 +56,15 @@ __device__ __forceinline__ uint32_t pack2<__half>(float2 f) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 8 values of a row as they lie in memory: zeros past its end.
-template <class T, bool kVec>
+// 8 neighbouring values of a row as they lie in memory.
+template <class T>
 struct Raw {
-  uint4 v[sizeof(T) / 2];  // kVec
-  T s[8];                  // else
-  __device__ __forceinline__ void load(const T *row, int c0, int lane, int dim) {
-    if constexpr (kVec) {
-      const int c = c0 + 8 * lane;
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *p, bool in) {  // zeros past the row's end
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        v[i] = c < dim ? reinterpret_cast<const uint4 *>(row + c)[i] : make_uint4(0, 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<false>(c0, lane, e);
-        s[e] = c < dim ? row[c] : from_f32<T>(0.f);
-      }
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = in ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ float2 pair(int i) const {
-    if constexpr (!kVec) return make_float2(to_f32(s[2 * i]), to_f32(s[2 * i + 1]));
     const uint4 u = v[sizeof(T) == 4 ? i / 2 : 0];
     if constexpr (sizeof(T) == 4)
       return i & 1 ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w)) : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
@@ -90,31 +73,27 @@ struct Raw {
   }
 };
 
-template <class T, bool kVec>
-__device__ __forceinline__ void store8(T *row, int c0, int lane, int dim, const float2 (&f)[4]) {
-  if constexpr (kVec) {
-    const int c = c0 + 8 * lane;
-    if (c >= dim) return;
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float4 *>(row + c)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      reinterpret_cast<float4 *>(row + c)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-    } else {
-      *reinterpret_cast<uint4 *>(row + c) = make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
-    }
+template <class T>
+__device__ __forceinline__ void store8(T *p, const float2 (&f)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (column<false>(c0, lane, e) < dim) row[column<false>(c0, lane, e)] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
   }
 }
+__device__ __forceinline__ void store8_e4m3(void *p, const float2 (&f)[4]) {
+  unsigned b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __nv_cvt_float2_to_fp8x2(f[i], __NV_SATFINITE, __NV_E4M3);
+  *static_cast<uint2 *>(p) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
 
-// f *= weight at this lane's columns.  wide: the weight is fp32 and 16-byte aligned.
-template <bool kVec>
-__device__ __forceinline__ void times_weight(const mrf_rms_norm_args &a, bool wide, int c0, int lane, float2 (&f)[4]) {
+// f *= the weight at columns c .. c + 7 (inside the row).  wide: the weight is fp32 and 16-byte aligned.
+__device__ __forceinline__ void times_weight(const mrf_rms_norm_args &a, bool wide, int c, float2 (&f)[4]) {
   if (!a.weight) return;
-  if (kVec && wide) {
-    if (c0 + 8 * lane >= a.dim) return;
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.weight) + c0 + 8 * lane);
+  if (wide) {
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.weight) + c);
     const float4 u = __ldg(p), v = __ldg(p + 1);
     f[0] = __fmul2_rn(f[0], make_float2(u.x, u.y));
     f[1] = __fmul2_rn(f[1], make_float2(u.z, u.w));
@@ -122,11 +101,8 @@ __device__ __forceinline__ void times_weight(const mrf_rms_norm_args &a, bool wi
     f[3] = __fmul2_rn(f[3], make_float2(v.z, v.w));
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<kVec>(c0, lane, e);
-      float &x = e & 1 ? f[e / 2].y : f[e / 2].x;
-      if (c < a.dim) x *= load_any(a.weight, a.weight_dtype, c);
-    }
+    for (int i = 0; i < 4; ++i)
+      f[i] = __fmul2_rn(f[i], make_float2(load_any(a.weight, a.weight_dtype, c + 2 * i), load_any(a.weight, a.weight_dtype, c + 2 * i + 1)));
   }
 }
 
@@ -158,8 +134,36 @@ struct Plan {
   int log2_group;   // of a.group
 };
 
-// Any shape: kWarpRow: a warp a row; else a block a row.
-template <class T, int V, bool kWarpRow, bool kVec>
+// s of a row with this sum of squares.  clamp: 1 / max(sqrt(mean), eps) = min(1 / sqrt(mean), 1 / eps); a NaN stays.
+__device__ __forceinline__ float row_factor(const mrf_rms_norm_args &a, const Plan &plan, float ss) {
+  const float mean = ss * plan.inv_dim;
+  const float s = rsqrtf(a.clamp ? mean : mean + a.eps);
+  return a.clamp && s > plan.inv_eps ? plan.inv_eps : s;
+}
+
+// An 8-bit group whose largest |h w| is m: scale = s m / 448 and code = h w * (448 / m); s drops out of the codes.
+struct Code {
+  float up, f;  // code = (h w * up) * f
+};
+__device__ __forceinline__ float code_scale(float s, float m) { return s * m * (1.f / 448.f); }
+__device__ __forceinline__ Code code_factor(float s, float m) {
+  const float scaled = s * m;
+  if (scaled > 0.f && m > 1e-30f && m < 1e30f) return {1.f, __fdividef(448.f, m)};  // (within 2 units in the last place)
+  // a scale of 0 gives codes 0, a NaN one NaN; where the quotient would leave fp32's range h w moves first
+  if (scaled == 0.f || scaled != scaled) return {1.f, scaled};
+  const float up = m < 1.f ? 0x1p90f : 0x1p-30f;
+  return {up, 448.f / (m * up)};
+}
+__device__ __forceinline__ void to_codes(float2 (&h)[4], Code c) {
+  if (c.up != 1.f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __fmul2_rn(h[i], make_float2(c.up, c.up));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __fmul2_rn(h[i], make_float2(c.f, c.f));
+}
+
+// Rows in 16-byte pieces held in registers, V vectors of 8 a thread.  kWarpRow: a warp a row; else a block a row.
+template <class T, int V, bool kWarpRow>
 __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf_rms_norm_args a, const Plan plan) {
   __shared__ float red[2][2][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -169,14 +173,14 @@ __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf
   const long long step = kWarpRow ? gridDim.x * (long long)warps : gridDim.x;
   int buf = 0;
   for (long long r = kWarpRow ? blockIdx.x * (long long)warps + warp : blockIdx.x; r < a.rows; r += step, buf ^= 1) {
-    auto first_column = [&](int v) { return 256 * (kWarpRow ? v : v * warps + warp); };
+    auto column = [&](int v) { return 256 * (kWarpRow ? v : v * warps + warp) + 8 * lane; };
     float2 h[V][4];
     {
-      Raw<T, kVec> xr[V], rr[V];
+      Raw<T> xr[V], rr[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        xr[v].load(x + r * a.x_stride, first_column(v), lane, a.dim);
-        if (res) rr[v].load(res + r * a.residual_stride, first_column(v), lane, a.dim);
+        xr[v].load(x + r * a.x_stride + column(v), column(v) < a.dim);
+        if (res) rr[v].load(res + r * a.residual_stride + column(v), column(v) < a.dim);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -188,9 +192,10 @@ __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf
     for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s2 = __ffma2_rn(h[v][i], h[v][i], s2);
-      if (a.residual_out)
-        store8<T, kVec>(static_cast<T *>(a.residual_out) + r * a.residual_out_stride, first_column(v), lane, a.dim, h[v]);
-      times_weight<kVec>(a, plan.wide, first_column(v), lane, h[v]);
+      if (column(v) < a.dim) {
+        if (a.residual_out) store8<T>(static_cast<T *>(a.residual_out) + r * a.residual_out_stride + column(v), h[v]);
+        times_weight(a, plan.wide, column(v), h[v]);
+      }
     }
     // the row's sum of squares and, for one scale a row, its largest |h w|
     float ss = s2.x + s2.y, top = 0.f;
@@ -211,76 +216,117 @@ __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf
       if (row_scale)
         for (int i = 0; i < warps; ++i) top = max_nan(top, red[buf][1][i]);
     }
-    // clamp: 1 / max(sqrt(mean), eps) = min(1 / sqrt(mean), 1 / eps), a NaN kept
-    const float mean = ss * plan.inv_dim;
-    float s = a.clamp ? rsqrtf(mean) : rsqrtf(mean + a.eps);
-    if (a.clamp && s > plan.inv_eps) s = plan.inv_eps;
-    if (!quant) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(s, s));
-        store8<T, kVec>(static_cast<T *>(a.out) + r * a.out_stride, first_column(v), lane, a.dim, h[v]);
-      }
-      continue;
-    }
-    // scale = s max |h w| / 448 over the group, code = h w * (448 / max |h w|): s drops out of the codes.
-    // A scale of 0 gives codes 0, a NaN one NaN; below 1e-30 the quotient would pass fp32, so both move up.
-    if (row_scale && lane == 0 && (kWarpRow || warp == 0)) a.scales[r] = s * top * (1.f / 448.f);
-    auto factor = [&](float m) {
-      const float scaled = s * m, up = m < 1e-30f ? 0x1p90f : 1.f;
-      return scaled == 0.f ? make_float2(0.f, 0.f) : scaled != scaled ? make_float2(scaled, scaled) : make_float2(up, 448.f / (m * up));
-    };
-    uint8_t *o = static_cast<uint8_t *>(a.out) + r * a.out_stride;
+    const float s = row_factor(a, plan, ss);
+    if (row_scale && lane == 0 && (kWarpRow || warp == 0)) a.scales[r] = code_scale(s, top);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c0 = first_column(v);
-      if (c0 >= a.dim) break;
-      if (kVec || row_scale) {
+      const int c = column(v);
+      if (c - 8 * lane >= a.dim) break;
+      if (!quant) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(s, s));
+        if (c < a.dim) store8<T>(static_cast<T *>(a.out) + r * a.out_stride + c, h[v]);
+      } else {
         float m = top;
         if (!row_scale) {  // group / 8 neighbouring lanes
           m = warp_max(max8(0.f, h[v]), a.group / 8);
-          const int c = c0 + 8 * lane;
-          if (c < a.dim && (lane & (a.group / 8 - 1)) == 0) a.scales[r * groups + (c >> plan.log2_group)] = s * m * (1.f / 448.f);
+          if (c < a.dim && (lane & (a.group / 8 - 1)) == 0) a.scales[r * groups + (c >> plan.log2_group)] = code_scale(s, m);
         }
-        const float2 f = factor(m);
-        if (f.x > 1.f)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(f.x, f.x));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(f.y, f.y));
-      } else {  // group / 32 values of every lane
-        const int n = a.group / 32;
-        float gm[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float m = warp_max(fabsf(e & 1 ? h[v][e / 2].y : h[v][e / 2].x), 32);
-          gm[e] = e % n ? max_nan(gm[e ? e - 1 : 0], m) : m;
-        }
-#pragma unroll
-        for (int e = 6; e >= 0; --e)
-          if ((e + 1) % n) gm[e] = gm[e + 1];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (lane == 0 && e % n == 0 && c0 + 32 * e < a.dim)
-            a.scales[r * groups + ((c0 + 32 * e) >> plan.log2_group)] = s * gm[e] * (1.f / 448.f);
-          const float2 f = factor(gm[e]);
-          float &q = e & 1 ? h[v][e / 2].y : h[v][e / 2].x;
-          q = q * f.x * f.y;
-        }
-      }
-      unsigned short b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = __nv_cvt_float2_to_fp8x2(h[v][i], __NV_SATFINITE, __NV_E4M3);
-      if constexpr (kVec) {
-        const int c = c0 + 8 * lane;
-        if (c < a.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(b[0] | (unsigned)b[1] << 16, b[2] | (unsigned)b[3] << 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (column<false>(c0, lane, e) < a.dim) o[column<false>(c0, lane, e)] = (uint8_t)(b[e / 2] >> (8 * (e & 1)));
+        to_codes(h[v], code_factor(s, m));
+        if (c < a.dim) store8_e4m3(static_cast<uint8_t *>(a.out) + r * a.out_stride + c, h[v]);
       }
     }
+  }
+}
+
+// Rows whose width, stride or address allows no 16-byte pieces: h w in fp32 in shared memory, value by value in
+// coalesced order; a team of a warp (kWarpRow) or a block for each row.
+// 16000 x 4097 with a residual and one scale per 128 values 272 us, 20000 x 131 16 us: 1.7 and 1.2 TB/s.
+constexpr int kBatch = 4;  // loads in flight before the first store (8: 330 us and 15 us)
+template <class T, bool kWarpRow>
+__global__ void __launch_bounds__(256) rms_norm_odd_kernel(const mrf_rms_norm_args a, const Plan plan) {
+  extern __shared__ float odd_rows[];
+  __shared__ float red[2][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int me = kWarpRow ? lane : threadIdx.x, team = kWarpRow ? 32 : blockDim.x;
+  float *row = odd_rows + (kWarpRow ? warp * a.dim : 0);
+  const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+  const bool quant = a.out_dtype == MRF_DTYPE_E4M3;
+  auto team_sync = [&]() {
+    if constexpr (kWarpRow) __syncwarp();
+    else __syncthreads();
+  };
+  // over the team's threads
+  auto reduce = [&](float v, bool sum) {
+    for (int o = 16; o; o >>= 1) {
+      const float u = __shfl_xor_sync(0xffffffffu, v, o);
+      v = sum ? v + u : max_nan(v, u);
+    }
+    if constexpr (!kWarpRow) {
+      __syncthreads();
+      if (lane == 0) red[sum][warp] = v;
+      __syncthreads();
+      v = red[sum][0];
+      for (int i = 1; i < warps; ++i) v = sum ? v + red[sum][i] : max_nan(v, red[sum][i]);
+    }
+    return v;
+  };
+  const long long step = kWarpRow ? gridDim.x * (long long)warps : gridDim.x;
+  for (long long r = kWarpRow ? blockIdx.x * (long long)warps + warp : blockIdx.x; r < a.rows; r += step) {
+    float ss = 0.f, top = 0.f;
+    const T *xr = x + r * a.x_stride, *rr = res ? res + r * a.residual_stride : nullptr;
+    T *ho = a.residual_out ? static_cast<T *>(a.residual_out) + r * a.residual_out_stride : nullptr;
+    for (int j0 = me; j0 < a.dim; j0 += kBatch * team) {
+      T xs[kBatch], rs[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = j0 + i * team;
+        const bool in = j < a.dim;
+        xs[i] = in ? xr[j] : from_f32<T>(0.f);
+        rs[i] = in && rr ? rr[j] : from_f32<T>(0.f);
+        w[i] = in && a.weight ? load_any(a.weight, a.weight_dtype, j) : 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = j0 + i * team;
+        if (j >= a.dim) break;
+        float h = to_f32(xs[i]) + to_f32(rs[i]);
+        if (ho) ho[j] = from_f32<T>(h);
+        ss = fmaf(h, h, ss);
+        h *= w[i];
+        top = max_nan(top, fabsf(h));
+        row[j] = h;
+      }
+    }
+    const float s = row_factor(a, plan, reduce(ss, true));
+    if (!quant) {
+      T *o = static_cast<T *>(a.out) + r * a.out_stride;
+#pragma unroll 4
+      for (int j = me; j < a.dim; j += team) o[j] = from_f32<T>(row[j] * s);
+    } else {
+      uint8_t *o = static_cast<uint8_t *>(a.out) + r * a.out_stride;
+      if (a.group == 0) {
+        top = reduce(top, false);
+        if (me == 0) a.scales[r] = code_scale(s, top);
+        const Code c = code_factor(s, top);
+#pragma unroll 4
+        for (int j = me; j < a.dim; j += team) o[j] = __nv_cvt_float_to_fp8(row[j] * c.up * c.f, __NV_SATFINITE, __NV_E4M3);
+      } else {
+        team_sync();  // a group's values are other threads'
+        const int groups = (a.dim + a.group - 1) / a.group;
+        for (int g = kWarpRow ? 0 : warp; g < groups; g += kWarpRow ? 1 : warps) {
+          const int j0 = g * a.group, j1 = min(a.dim, j0 + a.group);
+          float m = 0.f;
+          for (int j = j0 + lane; j < j1; j += 32) m = max_nan(m, fabsf(row[j]));
+          m = warp_max(m, 32);
+          if (lane == 0) a.scales[r * groups + g] = code_scale(s, m);
+          const Code c = code_factor(s, m);
+          for (int j = j0 + lane; j < j1; j += 32) o[j] = __nv_cvt_float_to_fp8(row[j] * c.up * c.f, __NV_SATFINITE, __NV_E4M3);
+        }
+      }
+    }
+    team_sync();  // before the next row's values
   }
 }
 
@@ -336,7 +382,7 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
   for (int v = 0; v < 2; ++v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[v][i] = make_float2(1.f, 1.f);
-    times_weight<true>(a, plan.wide, 256 * (v * warps + warp), lane, w[v]);
+    if (v ? in1 : in0) times_weight(a, plan.wide, v ? c1 : c0, w[v]);
   }
   const int groups = kMode == 2 ? (a.dim + a.group - 1) / a.group : 1;
   float *scales = kMode == 0 ? nullptr : a.scales + first * groups;
@@ -347,7 +393,7 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
     float2 h[2][4], s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      Raw<T, true> xr, rr;
+      Raw<T> xr, rr;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         xr.v[i] = load_shared(at + (v * P + i) * pstep);
@@ -361,8 +407,8 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
     }
     if constexpr (kRes)
       if (res_out) {
-        if (in0) store8<T, true>(res_out, 0, 0, 1, h[0]);
-        if (in1) store8<T, true>(res_out + far, 0, 0, 1, h[1]);
+        if (in0) store8<T>(res_out, h[0]);
+        if (in1) store8<T>(res_out + far, h[1]);
         res_out += step * a.residual_out_stride;
       }
 #pragma unroll
@@ -393,19 +439,17 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    const float mean = ss * plan.inv_dim;
-    float s = rsqrtf(a.clamp ? mean : mean + a.eps);
-    if (a.clamp && s > plan.inv_eps) s = plan.inv_eps;
+    const float s = row_factor(a, plan, ss);
     if constexpr (kMode == 0) {
 #pragma unroll
       for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(s, s));
       T *o = reinterpret_cast<T *>(out);
-      if (in0) store8<T, true>(o, 0, 0, 1, h[0]);
-      if (in1) store8<T, true>(o + far, 0, 0, 1, h[1]);
+      if (in0) store8<T>(o, h[0]);
+      if (in1) store8<T>(o + far, h[1]);
     } else {
-      if (kMode == 1 && threadIdx.x == 0) scales[0] = s * top * (1.f / 448.f);
+      if (kMode == 1 && threadIdx.x == 0) scales[0] = code_scale(s, top);
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         float m = top;
@@ -417,26 +461,10 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
           if (plan.log2_group > 5) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
           if (plan.log2_group > 6) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
           const int c = v ? c1 : c0;
-          if (in && (c & (a.group - 1)) == 0) scales[c >> plan.log2_group] = s * m * (1.f / 448.f);
+          if (in && (c & (a.group - 1)) == 0) scales[c >> plan.log2_group] = code_scale(s, m);
         }
-        const float scaled = s * m;
-        float f = __fdividef(448.f, m);  // (within 2 units in the last place)
-        if (!(scaled > 0.f && m > 1e-30f && m < 1e30f)) {
-          // a scale of 0 gives codes 0, a NaN one NaN; where the quotient would leave fp32's range h w moves first
-          if (scaled == 0.f || scaled != scaled) {
-            f = scaled;
-          } else {
-            const float up = m < 1.f ? 0x1p90f : 0x1p-30f;
-            f = 448.f / (m * up);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[v][i] = __fmul2_rn(h[v][i], make_float2(up, up));
-          }
-        }
-        unsigned short b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[i] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(h[v][i], make_float2(f, f)), __NV_SATFINITE, __NV_E4M3);
-        if (in) *reinterpret_cast<uint2 *>(out + (v ? far : 0)) = make_uint2(b[0] | (unsigned)b[1] << 16, b[2] | (unsigned)b[3] << 16);
+        to_codes(h[v], code_factor(s, m));
+        if (in) store8_e4m3(out + (v ? far : 0), h[v]);
       }
       scales += step * groups;
     }
@@ -463,39 +491,47 @@ bool vec_ok(const void *p, long long rows, long long stride, int size) {
   return reinterpret_cast<uintptr_t>(p) % (n * size) == 0 && (rows <= 1 || stride % n == 0);
 }
 
-template <class T, bool kVec>
-cudaError_t launch(const mrf_rms_norm_args &a, cudaStream_t st) {
+template <class T>
+cudaError_t launch(const mrf_rms_norm_args &a, bool vec, cudaStream_t st) {
   Plan p;
   p.wide = a.weight_dtype == MRF_DTYPE_F32 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
   p.inv_dim = 1.f / (float)a.dim;
   p.inv_eps = std::min(1.f / a.eps, 3.4e38f);  // finite: a row of zeros stays zeros
   p.log2_group = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   const int chunks = (a.dim + 255) / 256;  // of 256 columns: a vector of each lane of a warp
-  const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs: more threads a row, shorter chains
-  if (chunks <= 2) {
+  const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs
+  if (!vec) {
+    // a warp a row up to 1024 columns, where there are rows for every warp (20000 x 131: 16 us against 52 with a
+    // block a row, x 1003: 98 and 148, in batches of one; but 300 x 131: 4.0 against 2.9)
+    if (chunks <= 4 && !few) {
+      const int smem = 8 * a.dim * (int)sizeof(float);
+      rms_norm_odd_kernel<T, true><<<(int)std::min<long long>((a.rows + 7) / 8, 148 * 8), 256, smem, st>>>(a, p);
+    } else {
+      const int smem = a.dim * (int)sizeof(float), blocks = std::max(1, std::min(8, 220 * 1024 / (smem + 1024)));
+      auto *k = rms_norm_odd_kernel<T, false>;
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+      if (e != cudaSuccess) return e;
+      k<<<(int)std::min<long long>(a.rows, 148 * blocks), 256, smem, st>>>(a, p);
+    }
+  } else if (chunks == 1) {  // a warp a row (40000 x 64: 10.7 us against 14.5 with blocks; x 256: 15.5 and 15.3)
     const int warps = few ? 1 : 8;
     const int grid = (int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 64 / warps);
-    if (chunks == 1) rms_norm_kernel<T, 1, true, kVec><<<grid, 32 * warps, 0, st>>>(a, p);
-    else rms_norm_kernel<T, 2, true, kVec><<<grid, 32 * warps, 0, st>>>(a, p);
-    return cudaGetLastError();
+    rms_norm_kernel<T, 1, true><<<grid, 32 * warps, 0, st>>>(a, p);
+  } else if (chunks == 2 && !few && a.rows <= 148 * 64) {
+    // a warp a row while every row finds a warp at once (4201 x 384: 3.4 us against 4.9 streamed, x 512: 3.8 and
+    // 5.0; 9472 x 384: 5.5 and 6.2; 40000 x 384: 24 and 20, so not there; 4201 x 1024: 6.3 and 5.5, nor there)
+    rms_norm_kernel<T, 2, true><<<(int)((a.rows + 7) / 8), 256, 0, st>>>(a, p);
+  } else if (few && chunks <= 8) {
+    // more threads a row and shorter chains, up to 2048 columns (1 x 1024: 2.3 us against 2.6; 592 rows: 3.0 and
+    // 3.15; 1 x 8192: 4.4 against 3.6, so not there)
+    rms_norm_kernel<T, 1, false><<<(int)a.rows, 32 * chunks, 0, st>>>(a, p);
+  } else if (chunks <= 32) {
+    const int mode = a.out_dtype != MRF_DTYPE_E4M3 ? 0 : a.group == 0 ? 1 : 2;
+    if (a.residual) return mode == 0 ? launch_stream<T, 0, true>(a, p, st) : mode == 1 ? launch_stream<T, 1, true>(a, p, st) : launch_stream<T, 2, true>(a, p, st);
+    return mode == 0 ? launch_stream<T, 0, false>(a, p, st) : mode == 1 ? launch_stream<T, 1, false>(a, p, st) : launch_stream<T, 2, false>(a, p, st);
+  } else {
+    rms_norm_kernel<T, 5, false><<<(int)std::min<long long>(a.rows, 148), 32 * ((chunks + 4) / 5), 0, st>>>(a, p);
   }
-  if (few && chunks <= 16) {
-    rms_norm_kernel<T, 1, false, kVec><<<(int)a.rows, 32 * chunks, 0, st>>>(a, p);
-    return cudaGetLastError();
-  }
-  if (chunks <= 32) {
-    if constexpr (kVec) {
-      if (!few) {
-        const int mode = a.out_dtype != MRF_DTYPE_E4M3 ? 0 : a.group == 0 ? 1 : 2;
-        if (a.residual) return mode == 0 ? launch_stream<T, 0, true>(a, p, st) : mode == 1 ? launch_stream<T, 1, true>(a, p, st) : launch_stream<T, 2, true>(a, p, st);
-        return mode == 0 ? launch_stream<T, 0, false>(a, p, st) : mode == 1 ? launch_stream<T, 1, false>(a, p, st) : launch_stream<T, 2, false>(a, p, st);
-      }
-    }
-    const int warps = (chunks + 1) / 2;
-    rms_norm_kernel<T, 2, false, kVec><<<(int)std::min<long long>(a.rows, 148 * (32 / warps)), 32 * warps, 0, st>>>(a, p);
-    return cudaGetLastError();
-  }
-  rms_norm_kernel<T, 5, false, kVec><<<(int)std::min<long long>(a.rows, 148), 32 * ((chunks + 4) / 5), 0, st>>>(a, p);
   return cudaGetLastError();
 }
 
@@ -507,9 +543,9 @@ cudaError_t launch_rms_norm(const mrf_rms_norm_args &a, cudaStream_t st) {
                    (!a.residual || vec_ok(a.residual, a.rows, a.residual_stride, size)) &&
                    (!a.residual_out || vec_ok(a.residual_out, a.rows, a.residual_out_stride, size)) &&
                    vec_ok(a.out, a.rows, a.out_stride, a.out_dtype == MRF_DTYPE_E4M3 ? 1 : size);
-  if (a.dtype == MRF_DTYPE_F32) return vec ? launch<float, true>(a, st) : launch<float, false>(a, st);
-  if (a.dtype == MRF_DTYPE_F16) return vec ? launch<__half, true>(a, st) : launch<__half, false>(a, st);
-  return vec ? launch<__nv_bfloat16, true>(a, st) : launch<__nv_bfloat16, false>(a, st);
+  if (a.dtype == MRF_DTYPE_F32) return launch<float>(a, vec, st);
+  if (a.dtype == MRF_DTYPE_F16) return launch<__half>(a, vec, st);
+  return launch<__nv_bfloat16>(a, vec, st);
 }
 
 }  // namespace mrf
