@@ -59,6 +59,10 @@ constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
 constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
+// Key blocks of an item that are still to be loaded when the next one is taken: late, so that the longest items, which
+// come first, do not also get the first of the rest (a prompt of 4096 tokens, 16 heads: 69 us, 86 when it is taken at
+// once), and early enough for the time that taking one needs.
+constexpr int kAhead = 4;
 constexpr int kItems = 1;            // ring of work items: the next one is taken when everybody has begun this one
 
 // One unit of an item.  Token i of the tile sees the first min(klen, lim0 + i) keys of its range.
@@ -438,12 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.chunk) tc::griddep_launch_dependents();  // combine_kernel
   constexpr uint32_t kOCol = 256, kOStep = 64 * VA;
 
-  // the n-th item, copied from the ring; false when there is none left or a wait expired
-  auto next_item = [&](int n, Item &it) {
+  // the n-th item, copied from the ring (release: and acknowledged); false when there is none left or a wait expired
+  auto next_item = [&](int n, Item &it, bool release = true) {
     if (!wait_item(item_full + n % kItems, (n / kItems) & 1, status, 50, abort)) return false;
     it = items[n % kItems];
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(item_empty + n % kItems);
+    if (release && lane == 0) tc::mbar_arrive(item_empty + n % kItems);
     return !it.last;
   };
 
@@ -519,8 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0, qn = 0;  // ring slots filled, q buffers filled
       const uint32_t q_bytes = (uint32_t)(a.TQ * a.G) * 128 * QA;
       bool ok = true;
-      for (int n = 0; ok && next_item(n, it); ++n) {
+      for (int n = 0; ok && next_item(n, it, false); ++n) {
         const int n0 = it.u[0].nblk, n1 = it.u[1].nblk;
+        // the acknowledgement lets the next item be taken: only when this one nears its end
+        const int near_end = max(0, 2 * (max(n0, n1) - kAhead));
+        if (lane == 0 && n0 + n1 == 0) tc::mbar_arrive(item_empty + n % kItems);
         if (lane == 0 && n0 + n1 > 0) {
           const int qb = qn % C::qbufs;
           if (!tc::mbar_wait(q_empty + qb, ((qn / C::qbufs) & 1) ^ 1, status, 52, abort)) ok = false;
@@ -552,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const int nmax = max(n0, n1);
           for (int e = 0; ok && e < 2 * nmax; ++e) {
+            if (e == near_end) tc::mbar_arrive(item_empty + n % kItems);
             if (it.shared || e < 2 * n0) ok = fill(0, e, it.shared ? nmax : n0);
             if (ok && !it.shared && e < 2 * n1) ok = fill(1, e, n1);
           }
@@ -997,20 +1005,23 @@ Split split_of(const mrf_attention_args &a) {
   // More units than SMs: only single tiles (new tokens) of long sequences whose lengths only the device knows,
   // where the longest would keep its SM while the others are done (32 sequences up to 8192 keys, 8 key
   // heads: 110 us against 142; up to 1024: 34 against 26).
-  if (blocks < 8 || units > (tiles > a.seqs || a.seqs == 1 || blocks < 32 ? sms : 4 * sms)) return {0, 1};
+  if (units > (tiles > a.seqs || a.seqs == 1 || blocks < 32 ? sms : 4 * sms)) return {0, 1};
   // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
   // about eight rounds if all were as long as the longest.
   long long wanted = a.seqs == 1 ? 2 * (sms / units) : 16 * sms / units;
-  // A range's output is written and read again in fp32, at about 5 TB/s, against about 2 us a key block:
+  // A range's output is written and read again in fp32, at about 2.5 TB/s, against about 2 us a key block:
   // the number of ranges where their sum is least.
-  const double bytes = (double)a.q_rows * a.heads * a.v_width * 8;
-  wanted = std::min<long long>(wanted, (long long)std::sqrt(blocks * 2.0 / (bytes / 5e6)));
+  const double range = (double)a.q_rows * a.heads * a.v_width * 8 / 2.5e6, block = 2.0;
+  wanted = std::min<long long>(wanted, (long long)std::sqrt(blocks * block / range));
   if (wanted < 2) return {0, 1};
   long long chunk = (blocks + wanted - 1) / wanted;
   // (several sequences, 4 up to 8192 keys: at least 1, 2, 3, 4 blocks a range 36, 32, 31, 34 us)
   chunk = std::max<long long>({chunk, a.seqs == 1 ? 1 : 3, (blocks + 127) / 128});
   const long long most = (blocks + chunk - 1) / chunk;
-  return most < 2 ? Split{0, 1} : Split{(int)(chunk * kKeys), (int)most};
+  // and only where they gain on one range; 4 us for the joining launch (one sequence, 8 key heads: a token after 1024
+  // keys 12 us against 22, 128 after 4000 34 and 65; a prompt of 1024 tokens would take 34 against 24)
+  if (chunk * block + most * range + 4 >= blocks * block) return {0, 1};
+  return {(int)(chunk * kKeys), (int)most};
 }
 
 bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
