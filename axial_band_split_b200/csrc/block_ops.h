@@ -41,7 +41,14 @@ __device__ __forceinline__ float load_any(const void *p, int dtype, long long i)
 // Each queues its kernels on st; the arguments have been checked (op_api.cu).
 cudaError_t launch_rms_norm(const mrf_rms_norm_args &a, cudaStream_t st);
 cudaError_t launch_rope(const mrf_rope_args &a, cudaStream_t st);
-// CUDA-core attention (k_attn_rows.cu): any type, width and stride.
+// How the keys of few tiles are split: the keys of a range (0: no splits) and the most ranges a sequence can
+// have.  A tile has `tokens` tokens for one of `sets` sets of heads and takes `block` us for 128 keys.
+struct AttentionSplit {
+  int chunk, most;
+};
+AttentionSplit attention_split(const mrf_attention_args &a, int tokens, long long sets, double block);
+// CUDA-core attention (k_attn_rows.cu): any type, width and stride; the workspace it needs.
+size_t attention_rows_workspace(const mrf_attention_args &a);
 cudaError_t launch_attention_rows(const mrf_attention_args &a, cudaStream_t st);
 // Tensor-core attention (k_attn_packed_tc.cu): whether it takes these arguments, the workspace it
 // needs for them, and its launches (false: a tensor map was refused and nothing was queued).

@@ -40,6 +40,17 @@
 // Key rows past a sequence's end belong to others or were never written: their scores are replaced
 // by -inf whatever they are, and their rows of v, whose product with a zero probability could still
 // be NaN, are zeroed in shared memory before the second product.
+//
+// Measured, against a copy of 6.57 TB/s and a matrix product of 1669 TFLOP/s on the same device:
+//   a causal prompt of 16384 tokens, 16 heads of 128 over 4   0.86 ms, 1.28 PFLOP/s, 0.77
+//   7 causal prompts of 200 to 4096 tokens, 32 over 8         0.30 to 0.34 ms, 0.9 to 1.0 PFLOP/s, 0.54 to 0.6
+//   8 x 1100 tokens both ways, 8 heads of 64                  44 to 47 us, 0.42 to 0.45 PFLOP/s
+//   a token of each of 32 sequences of 500 to 8191 keys       106 us, 5.0 TB/s, 0.76
+//   a token after 65536 keys                                  58 us, 4.6 TB/s, 0.70
+// A block of 128 keys costs both units together 3400 to 3700 clk, where its matrix instructions need 2800 with widths of
+// 128 and its exponentials, at 16 a clk and SM, 2048: each unit's row loads, maxima, conversions and stores stand beside its
+// exponentials.  With 64 those phases bound it, and an item's start and output (about 4000 clk each) weigh as much as a block
+// or two, as they do in short prompts.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -993,36 +1004,8 @@ int sm_count() {
 bool few_rows(const mrf_attention_args &a) { return a.q_rows * (a.heads / a.kv_heads) <= 32ll * a.seqs && a.heads / a.kv_heads <= 32; }
 int tile_tokens(const mrf_attention_args &a) { return (few_rows(a) ? 32 : kRows) / (a.heads / a.kv_heads); }
 
-// How keys are split when there are few tiles: the keys of a range (0: no splits) and the most ranges a
-// sequence can have.
-struct Split {
-  int chunk, most;
-};
-Split split_of(const mrf_attention_args &a) {
-  const int TQ = tile_tokens(a);
-  const long long tiles = std::max<long long>(a.seqs, (a.q_rows + TQ - 1) / TQ), units = tiles * a.kv_heads, sms = sm_count();
-  const long long keys = a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows, blocks = (keys + kKeys - 1) / kKeys;
-  // More units than SMs: only single tiles (new tokens) of long sequences whose lengths only the device knows,
-  // where the longest would keep its SM while the others are done (32 sequences up to 8192 keys, 8 key
-  // heads: 110 us against 142; up to 1024: 34 against 26).
-  if (units > (tiles > a.seqs || a.seqs == 1 || blocks < 32 ? sms : 4 * sms)) return {0, 1};
-  // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
-  // about eight rounds if all were as long as the longest.
-  long long wanted = a.seqs == 1 ? 2 * (sms / units) : 16 * sms / units;
-  // A range's output is written and read again in fp32, at about 2.5 TB/s, against about 2 us a key block:
-  // the number of ranges where their sum is least.
-  const double range = (double)a.q_rows * a.heads * a.v_width * 8 / 2.5e6, block = 2.0;
-  wanted = std::min<long long>(wanted, (long long)std::sqrt(blocks * block / range));
-  if (wanted < 2) return {0, 1};
-  long long chunk = (blocks + wanted - 1) / wanted;
-  // (several sequences, 4 up to 8192 keys: at least 1, 2, 3, 4 blocks a range 36, 32, 31, 34 us)
-  chunk = std::max<long long>({chunk, a.seqs == 1 ? 1 : 3, (blocks + 127) / 128});
-  const long long most = (blocks + chunk - 1) / chunk;
-  // and only where they gain on one range; 4 us for the joining launch (one sequence, 8 key heads: a token after 1024
-  // keys 12 us against 22, 128 after 4000 34 and 65; a prompt of 1024 tokens would take 34 against 24)
-  if (chunk * block + most * range + 4 >= blocks * block) return {0, 1};
-  return {(int)(chunk * kKeys), (int)most};
-}
+// (about 2 us a block: see the head of this file)
+AttentionSplit split_of(const mrf_attention_args &a) { return attention_split(a, tile_tokens(a), a.kv_heads, 2.0); }
 
 bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
 
@@ -1040,8 +1023,33 @@ bool attention_tc_takes(const mrf_attention_args &a) {
          mult8(a.q_rows, a.out_token_stride) && mult8(a.heads, a.out_head_stride);
 }
 
+AttentionSplit attention_split(const mrf_attention_args &a, int tokens, long long sets, double block) {
+  const long long tiles = std::max<long long>(a.seqs, (a.q_rows + tokens - 1) / tokens), units = tiles * sets, sms = sm_count();
+  const long long keys = a.max_k ? std::min(a.max_k, a.k_rows) : a.k_rows, blocks = (keys + kKeys - 1) / kKeys;
+  // More units than SMs: only single tiles (new tokens) of long sequences whose lengths only the device knows,
+  // where the longest would keep its SM while the others are done (32 sequences up to 8192 keys, 8 key
+  // heads: 110 us against 142; up to 1024: 34 against 26).
+  if (units > (tiles > a.seqs || a.seqs == 1 || blocks < 32 ? sms : 4 * sms)) return {0, 1};
+  // One sequence: as many equal ranges as give every SM one item (two units).  Several: smaller ranges,
+  // about eight rounds if all were as long as the longest.
+  long long wanted = a.seqs == 1 ? 2 * (sms / units) : 16 * sms / units;
+  // A range's output is written and read again in fp32, at about 2.5 TB/s, against the time of a key block:
+  // the number of ranges where their sum is least.
+  const double range = (double)a.q_rows * a.heads * a.v_width * 8 / 2.5e6;
+  wanted = std::min<long long>(wanted, (long long)std::sqrt(blocks * block / range));
+  if (wanted < 2) return {0, 1};
+  long long chunk = (blocks + wanted - 1) / wanted;
+  // (several sequences, 4 up to 8192 keys: at least 1, 2, 3, 4 blocks a range 36, 32, 31, 34 us)
+  chunk = std::max<long long>({chunk, a.seqs == 1 ? 1 : 3, (blocks + 127) / 128});
+  const long long most = (blocks + chunk - 1) / chunk;
+  // and only where they gain on one range; 4 us for the joining launch (one sequence, 8 key heads: a token after 1024
+  // keys 12 us against 22, 128 after 4000 34 and 65; a prompt of 1024 tokens would take 34 against 24)
+  if (chunk * block + most * range + 4 >= blocks * block) return {0, 1};
+  return {(int)(chunk * kKeys), (int)most};
+}
+
 size_t attention_tc_workspace(const mrf_attention_args &a) {
-  const Split s = split_of(a);
+  const AttentionSplit s = split_of(a);
   return s.chunk ? (size_t)s.most * a.q_rows * a.heads * (a.v_width + 1) * sizeof(float) : 0;
 }
 
@@ -1064,7 +1072,7 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   a.width = m.width;
   a.v_width = m.v_width;
   a.causal = m.causal != 0;
-  const Split split = split_of(m);
+  const AttentionSplit split = split_of(m);
   a.chunk = split.chunk;
   a.max_splits = split.most;
   a.scale = m.scale;

@@ -176,7 +176,7 @@ mrf_status mrf_attention_workspace(const mrf_attention_args *a, size_t *bytes) {
   if (!bytes) return op_fail(MRF_EINVAL, "mrf_attention_workspace: null bytes pointer");
   *bytes = 0;
   const mrf_status s = check_attention(a);
-  if (s == MRF_OK && a->q_rows > 0 && a->seqs > 0 && attention_tc_takes(*a)) *bytes = attention_tc_workspace(*a);
+  if (s == MRF_OK && a->q_rows > 0 && a->seqs > 0) *bytes = attention_tc_takes(*a) ? attention_tc_workspace(*a) : attention_rows_workspace(*a);
   return s;
 }
 
@@ -184,13 +184,12 @@ mrf_status mrf_attention(const mrf_attention_args *a, void *stream) {
   const mrf_status s = check_attention(a);
   if (s != MRF_OK || a->q_rows == 0 || a->seqs == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (attention_tc_takes(*a)) {
-    const size_t need = attention_tc_workspace(*a);
-    if (need > 0 && (!a->workspace || addr(a->workspace) % 16 || a->workspace_bytes < need))
-      return op_fail(MRF_EINVAL, "mrf_attention: the workspace must hold %zu bytes, 16-byte aligned", need);
-    cudaError_t e = cudaSuccess;
-    if (launch_attention_packed_tc(*a, st, &e)) return op_done(e, "mrf_attention");
-  }
+  const bool tc = attention_tc_takes(*a);
+  const size_t need = tc ? attention_tc_workspace(*a) : attention_rows_workspace(*a);
+  if (need > 0 && (!a->workspace || addr(a->workspace) % 16 || a->workspace_bytes < need))
+    return op_fail(MRF_EINVAL, "mrf_attention: the workspace must hold %zu bytes, 16-byte aligned", need);
+  cudaError_t e = cudaSuccess;
+  if (tc && launch_attention_packed_tc(*a, st, &e)) return op_done(e, "mrf_attention");
   return op_done(launch_attention_rows(*a, st), "mrf_attention");
 }
 

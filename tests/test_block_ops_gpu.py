@@ -286,6 +286,39 @@ def test_attention_fp32(causal):
     run(Shape([(1, 450), (20, 13)], 6, 2, 80, 96, F32, causal))
 
 
+@pytest.mark.parametrize("dtype,width,v_width", [(F32, 64, 64), (F32, 128, 128), (F32, 256, 256), (F32, 65, 67), (F16, 36, 36), (BF16, 250, 9)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_of_other_types_and_widths(dtype, width, v_width, causal):
+    """fp32, odd and wide heads: every size of tile, split keys, ends inside a step, heads that fill several tiles."""
+    run(Shape([(1, None), (63, None), (64, None), (65, None), (300, None)], 2, 2, width, v_width, dtype, causal))
+    run(Shape([(1, 64), (1, 65), (3, 1000), (0, 9), (2, 0), (1, 4001)], 8, 2, width, v_width, dtype, causal, max_k=4001))
+    run(Shape([(1, 9000)], 8, 1, width, v_width, dtype, causal))
+    run(Shape([(40, 3000)], 4, 2, width, v_width, dtype, causal))
+    run(Shape([(1, 100), (3, 5)], 300, 2, width, v_width, dtype, causal))
+
+
+def test_attention_of_other_types_in_many_sequences():
+    """Empty sequences between others, and a key bound that is too low for the ranges that it sizes."""
+    run(Shape([(n % 5, None) for n in range(333)], 4, 2, dtype=F32))
+    run(Shape([(0, 5)] * 40 + [(130, 2000)] + [(0, 0)] * 40 + [(1, 4097)], 2, 1, 128, 128, F32, max_k=4097))
+    run(Shape([(1, 6000), (1, 100), (2, 1025)], 8, 1, 128, 128, F32, max_k=1024))
+    run(Shape([(1, 6000)], 8, 1, 100, 36, BF16, max_k=1024))
+
+
+def test_attention_of_other_types_and_strides():
+    """Heads that start off 16 bytes, and rows of no sequence that hold NaN."""
+    for width, off in ((64, 1), (64, 4), (30, 2)):
+        s = Shape([(70, None), (1, None)], 4, 2, width, width, F32)
+        q, k, v, offsets, _, _, spans = make(s, 5)
+        wide = torch.full((q.shape[0], 8 * (width + off) + off), math.nan, device="cuda")
+        parts = wide[:, off:].unflatten(1, (8, width + off))[..., :width]
+        parts[:, :4], parts[:, 4:6], parts[:, 6:] = q, k[: q.shape[0]], v[: q.shape[0]]
+        n = sum(p[1] for p in spans)
+        parts[n:] = math.nan
+        out, lse = mrf.attention_packed(parts[:, :4], parts[:, 4:6], parts[:, 6:], offsets, return_lse=True)
+        check_attention(s, q, k, v, spans, out, lse, width**-0.5)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_long(causal):
     run(Shape([(2100, None), (1300, None)], 2, 1, 128, 128, BF16, causal))
