@@ -285,6 +285,16 @@ def _like(t, x, dtype, dev, shape, name):
     return st
 
 
+def _new_like(t, x):
+    """A new tensor in the order of x's heads and tokens, and its strides."""
+    y = t.empty_like(x)
+    st = y.stride()
+    if st[-1] != 1:  # x's rows overlap (windows over one signal): another dimension came out innermost
+        y = x.new_empty(x.shape)
+        st = y.stride()
+    return y, st
+
+
 def _vector(t, x, dev, count, name, wide=False):
     """`x` is a contiguous int32 (or int64 where `wide`) vector of `count` values on device `dev`."""
     if not isinstance(x, t.Tensor) or x.get_device() != dev or not (x.dtype == t.i32 or (wide and x.dtype == t.i64)):
@@ -415,8 +425,8 @@ def rope_table(part, theta=10000.0, scaling="none", factor=1.0, original=0, beta
     turns = np.zeros(max(1, min(part, 1024) // 2), np.uint64)
     scale = ctypes.c_float(0)
     _check(lib().mrf_rope_table(ctypes.byref(c), turns.ctypes.data_as(ctypes.c_void_p), ctypes.byref(scale)))
-    # (not waited for: the copy has left this memory when the call returns, and the stream orders its use)
-    return RopeTable(torch.from_numpy(turns.view(np.int64)).to(device, non_blocking=True), scale.value, part)
+    # (waited for, so that any stream may use it)
+    return RopeTable(torch.from_numpy(turns.view(np.int64)).to(device), scale.value, part)
 
 
 def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, stream=None):
@@ -438,14 +448,13 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     ks = kos = (0, 0, 1)
     kv_heads = k_ptr = k_out_ptr = 0
     if k is not None:
-        if k.dim() != 3:
-            raise MrfError(-2, f"k must be [tokens, kv_heads, width], got {tuple(k.shape)}")
+        if not isinstance(k, t.Tensor) or k.dim() != 3:
+            raise MrfError(-2, f"k must be a tensor [tokens, kv_heads, width], got {tuple(getattr(k, 'shape', ()))}")
         kv_heads = k.shape[1]
         k_shape = (tokens, kv_heads, width)
         ks = _like(t, k, dtype, dev, k_shape, "k")
         if k_out is None:
-            k_out = t.empty_like(k)
-            kos = k_out.stride()
+            k_out, kos = _new_like(t, k)
         else:
             kos = _like(t, k_out, dtype, dev, k_shape, "k_out")
         k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
@@ -455,8 +464,7 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     if not isinstance(table, RopeTable) or table.turns.get_device() != dev:
         raise MrfError(-1, f"table must come from rope_table on cuda:{dev}")
     if q_out is None:
-        q_out = t.empty_like(q)
-        qos = q_out.stride()
+        q_out, qos = _new_like(t, q)
     else:
         qos = _like(t, q_out, dtype, dev, shape, "q_out")
     status = (_lib or lib()).mrf_rope(_ROPE.pack(
@@ -485,6 +493,8 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
     if stream is not None or dev != t.device():
         with _scope(dev, stream):
             return attention_packed(q, k, v, q_offsets, k_start, k_len, max_k, causal, scale, out, return_lse)
+    if not isinstance(v, t.Tensor):
+        raise MrfError(-1, f"v must be a tensor, got {type(v).__name__}")
     dtype, shape, v_shape = q.dtype, q.shape, v.shape
     if len(shape) != 3 or len(v_shape) != 3:
         raise MrfError(-2, f"q and v must be [rows, heads, width], got {tuple(shape)} and {tuple(v_shape)}")
@@ -505,8 +515,10 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
         start_ptr, len_ptr = (k_start.data_ptr(), k_len.data_ptr()) if seqs else (8, 8)
     elif k_len is not None or k_start is not None:
         raise MrfError(-1, "k_start and k_len go together")
-    if out is None:
-        out = t.empty_like(q) if v_width == width else q.new_empty((q_rows, heads, v_width))
+    if out is None and v_width == width:
+        out, (o_st, o_sh, _) = _new_like(t, q)
+    elif out is None:
+        out = q.new_empty((q_rows, heads, v_width))
         o_st, o_sh, _ = out.stride()
     else:
         o_st, o_sh, _ = _like(t, out, dtype, dev, (q_rows, heads, v_width), "out")

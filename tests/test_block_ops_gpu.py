@@ -479,6 +479,33 @@ def test_refusals_of_the_binding():
             pytest.fail(f"call {i} was not refused")
 
 
+def test_windows_over_one_signal():
+    """Inputs whose rows overlap (token and head strides below the width) give new outputs of their own layout."""
+    signal = randn(gen(8), 64 * 9, dtype=F16)
+    for strides in ((1, 2, 1), (8, 16, 1), (0, 0, 1), (2, 1, 1)):
+        x = signal.as_strided((20, 2, 64), strides)
+        dense = x.clone(memory_format=torch.contiguous_format)
+        off, pos = torch.tensor([0, 20], device="cuda", dtype=torch.int32), torch.arange(20, device="cuda")
+        table = mrf.rope_table(64)
+        assert all(torch.equal(a, b) for a, b in zip(mrf.rope(x, x, pos, table), mrf.rope(dense, dense, pos, table)))
+        got, want = mrf.attention_packed(x, x, x, off), mrf.attention_packed(dense, dense, dense, off)
+        # (strides that are no multiples of 8 go to the CUDA cores, without the probabilities' rounding to fp16 and with
+        # sums in another order: each side is within half a step of its weights and of the output)
+        assert (got.float() - want.float()).abs().max() <= 4 * 2.0**-11 * dense.float().abs().max()
+        got, want = mrf.rms_norm(x[:, 0]).out.float(), mrf.rms_norm(dense[:, 0]).out.float()
+        assert ((got - want).abs() <= 2 * 2.0**-11 * want.abs() + 2.0**-24).all()  # (the sums' order may move a rounding)
+
+
+def test_refusals_of_what_is_no_tensor():
+    x = torch.zeros(4, 2, 64, device="cuda", dtype=F16)
+    off, table = torch.tensor([0, 4], device="cuda", dtype=torch.int32), mrf.rope_table(64)
+    for call in (lambda: mrf.attention_packed(x, x, None, off), lambda: mrf.attention_packed(x, None, x, off), lambda: mrf.attention_packed(None, x, x, off),
+                 lambda: mrf.attention_packed(x, x, x, [0, 4]), lambda: mrf.rope(x, 3, off, table), lambda: mrf.rms_norm([1.0]),
+                 lambda: mrf.rms_norm(x, residual=1.0)):
+        with pytest.raises(mrf.MrfError):
+            call()
+
+
 def test_other_streams():
     """Calls on side streams, given as torch streams, raw pointers or the current one, at the same time."""
     s = Shape([(200, None), (300, None)], 8, 2, 128, 128)
