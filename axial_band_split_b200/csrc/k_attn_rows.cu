@@ -15,6 +15,7 @@
 // of the multiply-adds' peak; shared memory bounds the rest); a token of each of 32 sequences of 500 to 2000 keys, 32
 // heads of 128 over 8 0.28 ms (1.2 TB/s).  (A warp a row with a key a lane: 20.5 ms and 2.7 ms.)
 #include <algorithm>
+#include <atomic>
 
 #include "block_ops.h"
 
@@ -323,7 +324,13 @@ template <class T, int RI, int NE>
 cudaError_t launch(const mrf_attention_args &a, const Tiles &g, cudaStream_t st) {
   const int smem = (int)sizeof(float) * (16 * RI * (g.ld + kPad) + kKeys * (g.ld + 64 * NE));
   auto *k = attention_rows_kernel<T, RI, NE>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return e;
   k<<<(unsigned)std::min<long long>(g.units, 1 << 30), 256, smem, st>>>(a, g);
   e = cudaGetLastError();

@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "block_ops.h"
 
@@ -473,13 +474,24 @@ __global__ void __launch_bounds__(512, 2) rms_norm_stream_kernel(const mrf_rms_n
   copy_wait<0>();
 }
 
+// Lets kernel K's launches have up to 200 KB of shared memory, once a device (asking takes longer than a launch's checks).
+template <auto *K>
+cudaError_t allow_smem() {
+  static std::atomic<unsigned long long> ready{0};  // devices that were asked
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && ready.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 template <class T, int kMode, bool kRes>
 cudaError_t launch_stream(const mrf_rms_norm_args &a, const Plan &p, cudaStream_t st) {
   auto *k = rms_norm_stream_kernel<T, kMode, kRes>;
   const int warps = ((a.dim + 255) / 256 + 1) / 2;
   const int smem = kAhead * (kRes ? 2 : 1) * 2 * (int)sizeof(T) / 2 * 16 * 32 * warps;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem<rms_norm_stream_kernel<T, kMode, kRes>>()) return e;
   const int blocks = std::max(1, std::min(32 / warps, 220 * 1024 / (smem + 1280)));  // on an SM, at 64 registers a thread
   k<<<(int)std::min<long long>(a.rows, 148 * blocks), 32 * warps, smem, st>>>(a, p);
   return cudaGetLastError();
@@ -509,8 +521,7 @@ cudaError_t launch(const mrf_rms_norm_args &a, bool vec, cudaStream_t st) {
     } else {
       const int smem = a.dim * (int)sizeof(float), blocks = std::max(1, std::min(8, 220 * 1024 / (smem + 1024)));
       auto *k = rms_norm_odd_kernel<T, false>;
-      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-      if (e != cudaSuccess) return e;
+      if (const cudaError_t e = allow_smem<rms_norm_odd_kernel<T, false>>()) return e;
       k<<<(int)std::min<long long>(a.rows, 148 * blocks), 256, smem, st>>>(a, p);
     }
   } else if (chunks == 1) {  // a warp a row (40000 x 64: 10.7 us against 14.5 with blocks; x 256: 15.5 and 15.3)
