@@ -1000,7 +1000,9 @@ int sm_count() {
   return n;
 }
 
-// Sequences whose queries fill no more than 32 rows of a tile on average (single new tokens) take tiles of 32.
+// Sequences whose queries fill no more than 32 rows of a tile on average (single new tokens) take tiles of 32 (32 tokens
+// over 500 to 8191 keys 106 us against 145 with 128 rows, 64 over 2000 92 and 116; with a piece of 256 more among them
+// 116 and 117).
 bool few_rows(const mrf_attention_args &a) { return a.q_rows * (a.heads / a.kv_heads) <= 32ll * a.seqs && a.heads / a.kv_heads <= 32; }
 int tile_tokens(const mrf_attention_args &a) { return (few_rows(a) ? 32 : kRows) / (a.heads / a.kv_heads); }
 

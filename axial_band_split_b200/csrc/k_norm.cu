@@ -149,7 +149,12 @@ struct Code {
 __device__ __forceinline__ float code_scale(float s, float m) { return s * m * (1.f / 448.f); }
 __device__ __forceinline__ Code code_factor(float s, float m) {
   const float scaled = s * m;
-  if (scaled > 0.f && m > 1e-30f && m < 1e30f) return {1.f, __fdividef(448.f, m)};  // (within 2 units in the last place)
+  if (scaled > 0.f && m > 1e-30f && m < 1e30f) {
+    // The quotient within 2 units in the last place and one step of Newton's method, q + (448 - q m) / m with 1 / m = q / 448:
+    // codes on or near a tie round as those of the exact quotient.
+    const float q = __fdividef(448.f, m);
+    return {1.f, fmaf(fmaf(-q, m, 448.f), q * (1.f / 448.f), q)};
+  }
   // a scale of 0 gives codes 0, a NaN one NaN; where the quotient would leave fp32's range h w moves first
   if (scaled == 0.f || scaled != scaled) return {1.f, scaled};
   const float up = m < 1.f ? 0x1p90f : 0x1p-30f;
