@@ -2,11 +2,14 @@
 //
 // Bound by memory: every value is read and written once.  A block takes a few tokens: it first
 // computes their cos and sin into shared memory (part / 2 pairs a token, whatever the number of
-// heads), then walks over (token, head, unit) with a unit of 8 pairs or 8 untouched values, in
-// 16-byte accesses; where widths, strides or addresses do not allow those a unit is one pair or value.
+// heads), then walks over (token, head, unit) with a unit of N pairs or 2 N untouched values.  N is the
+// most of 8, 4, 2 and 1 whose pieces divide half the turned part and fit strides and addresses: 40 heads of 80
+// with 40 turned take 54 us with N = 4, 185 with 1; of 96 with 24 turned 59 and 224; of 80 with 20 turned 88 (N = 2)
+// and 200.
 // 16384 tokens of 40 heads of 128 in bf16 (336 MB): 60 us, 5.6 TB/s, 0.85 of the measured copy (a pair a
 // thread with its own cos and sin: 288 us; a token a block: 75 us).
 #include <algorithm>
+#include <type_traits>
 
 #include "block_ops.h"
 
@@ -25,27 +28,34 @@ __device__ __forceinline__ float2 turn(unsigned long long phase, float scale) {
 }
 
 struct Shape {
-  int rot;     // units of one head that turn, of 8 pairs (or one)
-  int units;   // and all its units
+  int rot;     // units of one head that turn, of N pairs
+  int units;   // and all its units; the others copy 2 N values
   int tokens;  // of one block
 };
 
-template <class T>
-struct Raw {
-  T v[8];
+// N neighbouring values, in accesses of up to 16 bytes.
+template <class T, int N>
+struct Piece {
+  static constexpr int kBytes = N * (int)sizeof(T) < 16 ? N * (int)sizeof(T) : 16;
+  using Word = std::conditional_t<kBytes == 16, uint4, std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
+  alignas(16) T v[N];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(T) / kBytes; ++i) reinterpret_cast<Word *>(v)[i] = reinterpret_cast<const Word *>(p)[i];
+  }
+  __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(T) / kBytes; ++i) reinterpret_cast<Word *>(p)[i] = reinterpret_cast<const Word *>(v)[i];
+  }
 };
 template <class T>
-__device__ __forceinline__ void load8(const T *p, Raw<T> &r) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(r.v)[i] = reinterpret_cast<const uint4 *>(p)[i];
-}
-template <class T>
-__device__ __forceinline__ void store8(T *p, const Raw<T> &r) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(r.v)[i];
+__device__ __forceinline__ void turn_pair(T &a, T &b, float2 c) {
+  const float a0 = to_f32(a), b0 = to_f32(b);
+  a = from_f32<T>(a0 * c.x - b0 * c.y);
+  b = from_f32<T>(b0 * c.x + a0 * c.y);
 }
 
-template <class T, bool kVec>
+template <class T, int N>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const mrf_rope_args a, const Shape s) {
   __shared__ float2 table[kMaxPairs];
   const int half = a.part / 2, all_heads = a.heads + a.kv_heads;
@@ -71,85 +81,74 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const mrf_rope_args a, c
                  (isk ? tok * a.k_token_stride + h * a.k_head_stride : tok * a.q_token_stride + h * a.q_head_stride);
     T *y = static_cast<T *>(isk ? a.k_out : a.q_out) + (isk ? tok * a.k_out_token_stride + h * a.k_out_head_stride
                                                              : tok * a.q_out_token_stride + h * a.q_out_head_stride);
-    if constexpr (kVec) {
-      if (u < (unsigned)s.rot) {
-        const int i0 = a.interleaved ? 16 * u : 8 * u, i1 = a.interleaved ? i0 + 8 : i0 + half;
-        Raw<T> p, q;
-        load8(x + i0, p);
-        load8(x + i1, q);
-        const float2 *cs = table + t * half + 8 * u;
-        if (a.interleaved) {
+    Piece<T, N> p, q;
+    if (u < (unsigned)s.rot) {
+      const int i0 = a.interleaved ? 2 * N * u : N * u, i1 = a.interleaved ? i0 + N : i0 + half;
+      p.load(x + i0);
+      q.load(x + i1);
+      const float2 *cs = table + t * half + N * u;
+      if (a.interleaved && N > 1) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 c = cs[e], d = cs[e + 4];
-            const float p0 = to_f32(p.v[2 * e]), p1 = to_f32(p.v[2 * e + 1]), q0 = to_f32(q.v[2 * e]), q1 = to_f32(q.v[2 * e + 1]);
-            p.v[2 * e] = from_f32<T>(p0 * c.x - p1 * c.y);
-            p.v[2 * e + 1] = from_f32<T>(p1 * c.x + p0 * c.y);
-            q.v[2 * e] = from_f32<T>(q0 * d.x - q1 * d.y);
-            q.v[2 * e + 1] = from_f32<T>(q1 * d.x + q0 * d.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 c = cs[e];
-            const float a0 = to_f32(p.v[e]), b0 = to_f32(q.v[e]);
-            p.v[e] = from_f32<T>(a0 * c.x - b0 * c.y);
-            q.v[e] = from_f32<T>(b0 * c.x + a0 * c.y);
-          }
+        for (int e = 0; e < N / 2; ++e) {
+          turn_pair(p.v[2 * e], p.v[(2 * e + 1) % N], cs[e]);
+          turn_pair(q.v[2 * e], q.v[(2 * e + 1) % N], cs[e + N / 2]);
         }
-        store8(y + i0, p);
-        store8(y + i1, q);
       } else {
-        const int i0 = a.part + 8 * (u - s.rot);
-        Raw<T> p;
-        load8(x + i0, p);
-        store8(y + i0, p);
+#pragma unroll
+        for (int e = 0; e < N; ++e) turn_pair(p.v[e], q.v[e], cs[e]);
       }
-    } else if (u < (unsigned)half) {
-      const int i0 = a.interleaved ? 2 * u : u, i1 = a.interleaved ? i0 + 1 : i0 + half;
-      const float2 c = table[t * half + u];
-      const float a0 = to_f32(x[i0]), b0 = to_f32(x[i1]);
-      y[i0] = from_f32<T>(a0 * c.x - b0 * c.y);
-      y[i1] = from_f32<T>(b0 * c.x + a0 * c.y);
+      p.store(y + i0);
+      q.store(y + i1);
     } else {
-      y[u + half] = x[u + half];
+      const int i0 = a.part + 2 * N * (u - s.rot), i1 = i0 + N;
+      p.load(x + i0);
+      if (i1 < a.width) q.load(x + i1);
+      p.store(y + i0);
+      if (i1 < a.width) q.store(y + i1);
     }
   }
 }
 
-bool vec_ok(const void *p, long long n1, long long s1, long long n2, long long s2, int size) {
-  const int n = 16 / size;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (n1 <= 1 || s1 % n == 0) && (n2 <= 1 || s2 % n == 0);
+// A [n1, n2, .] tensor takes pieces of n values.
+bool takes(const void *p, long long n1, long long s1, long long n2, long long s2, int size, int n) {
+  const int bytes = std::min(16, n * size);
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (n1 <= 1 || s1 * size % bytes == 0) && (n2 <= 1 || s2 * size % bytes == 0);
 }
 
-template <class T>
-void launch(const mrf_rope_args &a, bool vec, bool in_place, cudaStream_t st) {
+template <class T, int N>
+void launch(const mrf_rope_args &a, cudaStream_t st) {
   Shape s;
-  s.rot = vec ? a.part / 16 : a.part / 2;
+  s.rot = a.part / 2 / N;
   // dimensions that do not turn are copied, unless they are where they should be
-  s.units = s.rot + (in_place ? 0 : vec ? (a.width - a.part) / 8 : a.width - a.part);
+  const bool in_place = a.q_out == a.q && (a.kv_heads == 0 || a.k_out == a.k);
+  s.units = s.rot + (in_place ? 0 : (a.width - a.part + 2 * N - 1) / (2 * N));
   // about 1024 units a block, as long as there are blocks enough for every SM
   const long long per = (long long)(a.heads + a.kv_heads) * s.units;
   long long t = std::max(1ll, std::min<long long>({1024 / per, a.tokens / (148 * 4), kMaxPairs / (a.part / 2)}));
   s.tokens = (int)t;
-  const int grid = (int)((a.tokens + t - 1) / t);
-  if (vec) rope_kernel<T, true><<<grid, kThreads, 0, st>>>(a, s);
-  else rope_kernel<T, false><<<grid, kThreads, 0, st>>>(a, s);
+  rope_kernel<T, N><<<(int)((a.tokens + t - 1) / t), kThreads, 0, st>>>(a, s);
+}
+template <class T>
+void launch(const mrf_rope_args &a, cudaStream_t st) {
+  constexpr int size = sizeof(T);
+  auto fits = [&](int n) {
+    return a.part / 2 % n == 0 && a.width % n == 0 && takes(a.q, a.tokens, a.q_token_stride, a.heads, a.q_head_stride, size, n) &&
+           takes(a.q_out, a.tokens, a.q_out_token_stride, a.heads, a.q_out_head_stride, size, n) &&
+           (a.kv_heads == 0 || (takes(a.k, a.tokens, a.k_token_stride, a.kv_heads, a.k_head_stride, size, n) &&
+                                takes(a.k_out, a.tokens, a.k_out_token_stride, a.kv_heads, a.k_out_head_stride, size, n)));
+  };
+  if (fits(8)) launch<T, 8>(a, st);
+  else if (fits(4)) launch<T, 4>(a, st);
+  else if (fits(2)) launch<T, 2>(a, st);
+  else launch<T, 1>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const mrf_rope_args &a, cudaStream_t st) {
-  const int size = a.dtype == MRF_DTYPE_F32 ? 4 : 2;
-  const bool vec = a.part % 16 == 0 && a.width % 8 == 0 &&
-                   vec_ok(a.q, a.tokens, a.q_token_stride, a.heads, a.q_head_stride, size) &&
-                   vec_ok(a.q_out, a.tokens, a.q_out_token_stride, a.heads, a.q_out_head_stride, size) &&
-                   (a.kv_heads == 0 || (vec_ok(a.k, a.tokens, a.k_token_stride, a.kv_heads, a.k_head_stride, size) &&
-                                        vec_ok(a.k_out, a.tokens, a.k_out_token_stride, a.kv_heads, a.k_out_head_stride, size)));
-  const bool in_place = a.q_out == a.q && (a.kv_heads == 0 || a.k_out == a.k);
-  if (a.dtype == MRF_DTYPE_F32) launch<float>(a, vec, in_place, st);
-  else if (a.dtype == MRF_DTYPE_F16) launch<__half>(a, vec, in_place, st);
-  else launch<__nv_bfloat16>(a, vec, in_place, st);
+  if (a.dtype == MRF_DTYPE_F32) launch<float>(a, st);
+  else if (a.dtype == MRF_DTYPE_F16) launch<__half>(a, st);
+  else launch<__nv_bfloat16>(a, st);
   return cudaGetLastError();
 }
 
