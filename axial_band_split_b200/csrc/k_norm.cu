@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "block_ops.h"
 
@@ -245,12 +246,25 @@ __global__ void __launch_bounds__(512, V <= 2 ? 2 : 1) rms_norm_kernel(const mrf
   }
 }
 
+// The codes of values j, j + step ... below n, two at a time.
+__device__ __forceinline__ void codes_of(const float *row, uint8_t *o, int j, int n, int step, Code c) {
+  for (; j < n; j += 2 * step) {
+    const bool two = j + step < n;
+    float2 v = make_float2(row[j], two ? row[j + step] : 0.f);
+    if (c.up != 1.f) v = __fmul2_rn(v, make_float2(c.up, c.up));
+    const unsigned b = __nv_cvt_float2_to_fp8x2(__fmul2_rn(v, make_float2(c.f, c.f)), __NV_SATFINITE, __NV_E4M3);
+    o[j] = (uint8_t)b;
+    if (two) o[j + step] = (uint8_t)(b >> 8);
+  }
+}
+
 // Rows whose width, stride or address allows no 16-byte pieces: h w in fp32 in shared memory, value by value in
 // coalesced order; a team of a warp (kWarpRow) or a block for each row.
-// 16000 x 4097 with a residual and one scale per 128 values 272 us, 20000 x 131 16 us: 1.7 and 1.2 TB/s.
-constexpr int kBatch = 4;  // loads in flight before the first store (8: 330 us and 15 us)
+// 16000 x 4097 with a residual and one scale per 128 values 195 us, 20000 x 1003 49 us, 20000 x 131 13 us: 2.4, 2.9 and
+// 1.4 TB/s, bound by the instructions that single values take.
+constexpr int kBatch = 8;  // loads of x and the residual each in flight (4: 16000 x 4097 30% slower; 16: twice as slow, spills)
 template <class T, bool kWarpRow>
-__global__ void __launch_bounds__(256) rms_norm_odd_kernel(const mrf_rms_norm_args a, const Plan plan) {
+__global__ void __launch_bounds__(256, 4) rms_norm_odd_kernel(const mrf_rms_norm_args a, const Plan plan) {
   extern __shared__ float odd_rows[];
   __shared__ float red[2][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -282,29 +296,49 @@ __global__ void __launch_bounds__(256) rms_norm_odd_kernel(const mrf_rms_norm_ar
     float ss = 0.f, top = 0.f;
     const T *xr = x + r * a.x_stride, *rr = res ? res + r * a.residual_stride : nullptr;
     T *ho = a.residual_out ? static_cast<T *>(a.residual_out) + r * a.residual_out_stride : nullptr;
-    for (int j0 = me; j0 < a.dim; j0 += kBatch * team) {
-      T xs[kBatch], rs[kBatch];
-      float w[kBatch];
+    // values j0, j0 + team ...; kFull: all of a batch lie in the row
+    auto batch = [&](int j0, auto full) {
+      constexpr bool kFull = decltype(full)::value;
+      T v[kBatch], u[kBatch];
+      float h[kBatch];
+      auto in = [&](int i) { return kFull || j0 + i * team < a.dim; };
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int j = j0 + i * team;
-        const bool in = j < a.dim;
-        xs[i] = in ? xr[j] : from_f32<T>(0.f);
-        rs[i] = in && rr ? rr[j] : from_f32<T>(0.f);
-        w[i] = in && a.weight ? load_any(a.weight, a.weight_dtype, j) : 1.f;
+      for (int i = 0; i < kBatch; ++i) v[i] = in(i) ? xr[j0 + i * team] : from_f32<T>(0.f);
+      if (rr) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) u[i] = in(i) ? rr[j0 + i * team] : from_f32<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) h[i] = to_f32(v[i]) + to_f32(u[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) h[i] = to_f32(v[i]);
       }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int j = j0 + i * team;
-        if (j >= a.dim) break;
-        float h = to_f32(xs[i]) + to_f32(rs[i]);
-        if (ho) ho[j] = from_f32<T>(h);
-        ss = fmaf(h, h, ss);
-        h *= w[i];
-        top = max_nan(top, fabsf(h));
-        row[j] = h;
+      for (int i = 0; i < kBatch; ++i) ss = fmaf(h[i], h[i], ss);
+      if (ho) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (in(i)) ho[j0 + i * team] = from_f32<T>(h[i]);
       }
-    }
+      auto weigh = [&](auto *w) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (in(i)) h[i] *= to_f32(w[j0 + i * team]);
+      };
+      if (!a.weight) {
+      } else if (a.weight_dtype == MRF_DTYPE_F32) weigh(static_cast<const float *>(a.weight));
+      else if (a.weight_dtype == MRF_DTYPE_F16) weigh(static_cast<const __half *>(a.weight));
+      else weigh(static_cast<const __nv_bfloat16 *>(a.weight));
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (in(i)) {
+          top = max_nan(top, fabsf(h[i]));
+          row[j0 + i * team] = h[i];
+        }
+    };
+    int j0 = me;
+    for (; j0 + (kBatch - 1) * team < a.dim; j0 += kBatch * team) batch(j0, std::true_type());
+    if (j0 < a.dim) batch(j0, std::false_type());
     const float s = row_factor(a, plan, reduce(ss, true));
     if (!quant) {
       T *o = static_cast<T *>(a.out) + r * a.out_stride;
@@ -316,19 +350,19 @@ __global__ void __launch_bounds__(256) rms_norm_odd_kernel(const mrf_rms_norm_ar
         top = reduce(top, false);
         if (me == 0) a.scales[r] = code_scale(s, top);
         const Code c = code_factor(s, top);
-#pragma unroll 4
-        for (int j = me; j < a.dim; j += team) o[j] = __nv_cvt_float_to_fp8(row[j] * c.up * c.f, __NV_SATFINITE, __NV_E4M3);
+        codes_of(row, o, me, a.dim, team, c);
       } else {
         team_sync();  // a group's values are other threads'
         const int groups = (a.dim + a.group - 1) / a.group;
         for (int g = kWarpRow ? 0 : warp; g < groups; g += kWarpRow ? 1 : warps) {
           const int j0 = g * a.group, j1 = min(a.dim, j0 + a.group);
           float m = 0.f;
-          for (int j = j0 + lane; j < j1; j += 32) m = max_nan(m, fabsf(row[j]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // (a group is 128 at most)
+            if (j0 + 32 * i + lane < j1) m = max_nan(m, fabsf(row[j0 + 32 * i + lane]));
           m = warp_max(m, 32);
           if (lane == 0) a.scales[r * groups + g] = code_scale(s, m);
-          const Code c = code_factor(s, m);
-          for (int j = j0 + lane; j < j1; j += 32) o[j] = __nv_cvt_float_to_fp8(row[j] * c.up * c.f, __NV_SATFINITE, __NV_E4M3);
+          codes_of(row, o, j0 + lane, j1, 32, code_factor(s, m));
         }
       }
     }
@@ -518,16 +552,16 @@ cudaError_t launch(const mrf_rms_norm_args &a, bool vec, cudaStream_t st) {
   const int chunks = (a.dim + 255) / 256;  // of 256 columns: a vector of each lane of a warp
   const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs
   if (!vec) {
-    // a warp a row up to 1024 columns, where there are rows for every warp (20000 x 131: 16 us against 52 with a
-    // block a row, x 1003: 98 and 148, in batches of one; but 300 x 131: 4.0 against 2.9)
-    if (chunks <= 4 && !few) {
-      const int smem = 8 * a.dim * (int)sizeof(float);
-      rms_norm_odd_kernel<T, true><<<(int)std::min<long long>((a.rows + 7) / 8, 148 * 8), 256, smem, st>>>(a, p);
+    // a warp a row up to 2048 columns where there are rows for every warp (20000 x 2001: 101 us against 153 with a block a row,
+    // x 131: 13 and 52; but 16000 x 4097: 286 and 195, and 300 x 131: 4.0 and 2.9)
+    if (chunks <= 8 && !few) {
+      const int warps = 4, smem = warps * a.dim * (int)sizeof(float);
+      if (const cudaError_t e = allow_smem<rms_norm_odd_kernel<T, true>>()) return e;
+      rms_norm_odd_kernel<T, true><<<(int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 64), 32 * warps, smem, st>>>(a, p);
     } else {
-      const int smem = a.dim * (int)sizeof(float), blocks = std::max(1, std::min(8, 220 * 1024 / (smem + 1024)));
-      auto *k = rms_norm_odd_kernel<T, false>;
+      const int smem = a.dim * (int)sizeof(float);
       if (const cudaError_t e = allow_smem<rms_norm_odd_kernel<T, false>>()) return e;
-      k<<<(int)std::min<long long>(a.rows, 148 * blocks), 256, smem, st>>>(a, p);
+      rms_norm_odd_kernel<T, false><<<(int)std::min<long long>(a.rows, 148 * 64), 256, smem, st>>>(a, p);
     }
   } else if (chunks == 1) {  // a warp a row (40000 x 64: 10.7 us against 14.5 with blocks; x 256: 15.5 and 15.3)
     const int warps = few ? 1 : 8;
