@@ -75,6 +75,24 @@ def test_norm_e4m3(dtype, rows, dim, group):
     within(r.residual, h, h.abs() * (block_ref.U32 + block_ref.half_step(dtype)) * 1.001 + 2.0**-25, "h")
 
 
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("rows,dim", [(700, 131), (613, 2047), (600, 2049), (20, 4097)])
+def test_norm_of_odd_widths(dtype, rows, dim):
+    """A warp and a block a row, whole batches of values and their ends, every kind of scale and of weight."""
+    g = gen(rows + dim)
+    x, res, w = randn(g, rows, dim, dtype=dtype), randn(g, rows, dim, dtype=dtype), 1 + 0.5 * randn(g, dim)
+    for group, residual, weight in ((0, res, w), (32, None, w.to(F16)), (64, res, None), (128, res, w.to(BF16))):
+        r = mrf.rms_norm(x, weight, 1e-6, residual, out_dtype=E4M3, group=group)
+        y, h = block_ref.rms_norm(x, weight, 1e-6, residual)
+        check_quant(r, y, group, dim)
+        r = mrf.rms_norm(x, weight, 1e-6, residual)
+        within(r.out, y, y.abs() * (block_ref.norm_slack(dim) + block_ref.half_step(dtype)) + 2.0**-25, "out")
+        if residual is not None:
+            within(r.residual, h, h.abs() * (block_ref.U32 + block_ref.half_step(dtype)) * 1.001 + 2.0**-25, "h")
+            again = mrf.rms_norm(x.clone(), weight, 1e-6, residual, residual_out=residual.clone())
+            assert torch.equal(again.out, r.out) and torch.equal(again.residual, r.residual)
+
+
 def test_norm_zero_nan_and_infinity():
     x = torch.zeros(4, 256, device="cuda", dtype=BF16)
     x[1, 5] = math.nan
@@ -155,6 +173,23 @@ def test_rope_far_positions_wide():
     size = block_ref.rope_slack(a.abs() + b.abs())
     within(got[..., 0::2], a * c - b * s, size)
     within(got[..., 1::2], b * c + a * s, size)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("width,part", [(80, 40), (96, 24), (32, 8), (28, 8), (44, 40), (6, 4), (18, 12), (48, 16), (24, 16)])
+def test_rope_pieces(dtype, interleaved, width, part):
+    """Parts whose half is a multiple of 8, 4, 2 or 1, an odd number of pieces that do not turn, and rows that start off 16 bytes."""
+    g = gen(width + part)
+    pos = torch.arange(700, device="cuda", dtype=torch.int32)
+    table = mrf.rope_table(part)
+    f, mul = block_ref.rope_frequencies(part)
+    for lead in (0, 1, 2, 4):
+        row = randn(g, 700, lead + 5 * width + (-(lead + 5 * width)) % 8, dtype=dtype)
+        view = row[:, lead : lead + 5 * width].unflatten(1, (5, width))
+        for x, y in zip((view[:, :4], view[:, 4:]), mrf.rope(view[:, :4], view[:, 4:], pos, table, interleaved)):
+            ref, size = block_ref.rope(x, pos, f, mul, interleaved)
+            within(y, ref, block_ref.rope_slack(size) + block_ref.half_step(dtype) * ref.abs() * 1.01 + (size > 0) * 2.0**-25)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
