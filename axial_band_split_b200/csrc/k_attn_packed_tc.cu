@@ -57,12 +57,13 @@
 
 #include "block_ops.h"
 #include "gemm_tc.cuh"
+#include "packed_items.cuh"
 #include "tc_ptx.cuh"
 
 namespace mrf {
 namespace {
 
-constexpr int kRows = 128, kKeys = 128, kHalf = 64;
+constexpr int kRows = 128, kHalf = 64;
 constexpr int kLate = 32;           // keys of P's second half whose exponentials run before the first half is handed over
 constexpr int kAtom = kRows * 128;  // 64 16-bit values of 128 rows
 constexpr int kThreads = 384;
@@ -75,22 +76,6 @@ constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exce
 // once), and early enough for the time that taking one needs.
 constexpr int kAhead = 4;
 constexpr int kItems = 1;            // ring of work items: the next one is taken when everybody has begun this one
-
-// One unit of an item.  Token i of the tile sees the first min(klen, lim0 + i) keys of its range.
-struct Unit {
-  int q_row, ntok;   // the tile's first query row, its tokens (0: no unit)
-  int kvh;
-  int k_row, klen;   // the range's first key row, its keys
-  int lim0;
-  int nblk;          // key blocks that any of its tokens sees
-  int split;
-};
-struct Item {
-  Unit u[2];
-  int shared;  // both units read the same key blocks
-  int partial; // one key range of several: outputs go to the workspace
-  int last;    // no more items
-};
 
 // kFew: tiles of 32 rows (new tokens).  The matrix instructions still have 128 rows, but only 32 are stored:
 // unit t's are rows 32 t .. 32 t + 31 of an area of 64, which both units' operands start at, and what the
@@ -119,15 +104,13 @@ struct Cfg {
   static_assert(p + kAtom <= bar && q + qbufs * qbuf + kAtom <= bar, "operands of 128 rows stay inside");
 };
 
-struct Args {
+struct Args : Batch {
   void *out;
   float *lse;         // or null
   float *part;        // splits: [split][row * heads + head][v_width], then their log2 sums
   float *part_lse;
-  const int32_t *q_offsets, *k_start, *k_len;
   long long out_token_stride, out_head_stride;
-  int q_rows, k_rows, seqs, heads, kv_heads, G, TQ, width, v_width, causal;
-  int chunk, max_splits;  // keys of a range (0: no splits), ranges that the workspace holds
+  int heads, G, width, v_width;
   float scale, scale_log2;
 };
 
@@ -279,80 +262,6 @@ __device__ __forceinline__ bool wait_item(uint64_t *bar, uint32_t parity, unsign
   return true;
 }
 
-// ------------------------------------------------------------------ sequences and items
-struct Seq {
-  int q0, nq, k0, nk;
-};
-// Sequence b's rows, held to the tensors' whatever the offsets say.
-__device__ __forceinline__ Seq load_seq(const Args &a, int b) {
-  Seq s;
-  s.q0 = min(max(a.q_offsets[b], 0), a.q_rows);
-  s.nq = min(max(a.q_offsets[b + 1], s.q0), a.q_rows) - s.q0;
-  if (a.k_len) {
-    s.k0 = min(max(a.k_start[b], 0), a.k_rows);
-    s.nk = min(max(a.k_len[b], 0), a.k_rows - s.k0);
-  } else {
-    s.k0 = s.q0;
-    s.nk = s.nq;
-  }
-  return s;
-}
-// The keys of a sequence's ranges: whole blocks, more of them than `chunk` only where the workspace would not
-// hold the ranges (max_k was too low).
-__device__ __forceinline__ int range_keys(const Args &a, int nk) {
-  if (a.chunk == 0) return nk;
-  const int least = ((nk + a.max_splits - 1) / a.max_splits + kKeys - 1) / kKeys * kKeys;
-  return max(a.chunk, least);
-}
-__device__ __forceinline__ int range_count(const Args &a, int nk) {
-  return a.chunk == 0 ? 1 : max(1, (nk - 1) / range_keys(a, nk) + 1);
-}
-__device__ __forceinline__ long long seq_items(const Args &a, const Seq &s) {
-  const int nt = (s.nq + a.TQ - 1) / a.TQ, ns = range_count(a, s.nk);
-  if (ns > 1) return (long long)nt * a.kv_heads * ((ns + 1) / 2);
-  return (long long)a.kv_heads * (nt / 2) + (nt & 1) * ((a.kv_heads + 1) / 2);
-}
-__device__ __forceinline__ Unit make_unit(const Args &a, const Seq &s, int tile, int kvh, int split) {
-  Unit u;
-  const int t0 = tile * a.TQ, chunk = range_keys(a, s.nk);
-  const int r0 = (int)min((long long)split * chunk, (long long)s.nk);
-  u.q_row = s.q0 + t0;
-  u.ntok = min(a.TQ, s.nq - t0);
-  u.kvh = kvh;
-  u.k_row = s.k0 + r0;
-  u.klen = min(s.nk - r0, chunk);
-  u.lim0 = a.causal ? (t0 - s.nq) + 1 + (s.nk - r0) : u.klen;
-  u.nblk = (max(0, min(u.klen, u.lim0 + u.ntok - 1)) + kKeys - 1) / kKeys;
-  u.split = split;
-  return u;
-}
-__device__ __forceinline__ Item make_item(const Args &a, const Seq &s, long long r) {
-  Item it;
-  const int nt = (s.nq + a.TQ - 1) / a.TQ, ns = range_count(a, s.nk);
-  it.last = 0;
-  it.shared = 0;
-  it.partial = ns > 1;
-  if (ns > 1) {
-    const int js = (ns + 1) / 2, j = (int)(r % js), th = (int)(r / js);
-    const int tile = nt - 1 - th / a.kv_heads, kvh = th % a.kv_heads;
-    it.u[0] = make_unit(a, s, tile, kvh, 2 * j);
-    it.u[1] = make_unit(a, s, tile, kvh, 2 * j + 1);
-    if (2 * j + 1 >= ns) it.u[1].ntok = it.u[1].nblk = 0;
-  } else if (r < (long long)a.kv_heads * (nt / 2)) {
-    const int tile = (nt & 1) + 2 * (nt / 2 - 1 - (int)(r / a.kv_heads)), kvh = (int)(r % a.kv_heads);
-    it.shared = 1;
-    it.u[0] = make_unit(a, s, tile, kvh, 0);
-    it.u[1] = make_unit(a, s, tile + 1, kvh, 0);
-  } else {
-    const int kvh = 2 * (int)(r - (long long)a.kv_heads * (nt / 2));
-    it.u[0] = make_unit(a, s, 0, kvh, 0);
-    it.u[1] = it.u[0];
-    it.u[1].kvh = kvh + 1;
-    if (kvh + 1 >= a.kv_heads) it.u[1].ntok = it.u[1].nblk = 0;
-  }
-  return it;
-}
-
 // A stream of n key blocks in the order of its use, the elements of block j: with wide v K0 V0 K1 V1 ...,
 // else K0 K1 V0 K2 V1 ... V(n - 1).
 template <bool kOverlay>
@@ -466,13 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIo));
     if (warp == 11) {
       // ---------------- items: a running prefix sum over 32 sequences at a time
-      int base = 0;
-      long long before = 0, total = 0, incl = 0;  // 64 bits: wrong offsets may count rows many times
+      Walk walk = {};
+      long long incl = 0;
       Seq s = {};
       auto load = [&]() {
         long long cnt = 0;
-        if (base + lane < a.seqs) {
-          s = load_seq(a, base + lane);
+        if (walk.base + lane < a.seqs) {
+          s = load_seq(a, walk.base + lane);
           cnt = seq_items(a, s);
         }
         incl = cnt;
@@ -480,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long v = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += v;
         }
-        total = __shfl_sync(0xffffffffu, incl, 31);
+        walk.total = __shfl_sync(0xffffffffu, incl, 31);
       };
       load();
       long long it = blockIdx.x;
@@ -506,13 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (it < 0) break;
           }
-          while (base < a.seqs && it >= before + total) {
-            base += 32;
-            before += total;
-            load();
-          }
-          if (base >= a.seqs) continue;
-          const long long r = it - before;
+          if (!find_sequences(walk, a.seqs, it, load)) continue;
+          const long long r = it - walk.before;
           const int src = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
           Seq q;
           q.q0 = __shfl_sync(0xffffffffu, s.q0, src);
