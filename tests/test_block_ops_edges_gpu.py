@@ -1,0 +1,128 @@
+"""The block operators where their loops turn more than once, where offsets are wrong and where a graph captures the
+first call, against their formulas in 64 bits with the bounds that block_ref derives."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import block_ref
+from axial_band_split_b200 import mrf
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_block_ops_gpu import BF16, E4M3, F16, F32, check_quant, gen, randn, within  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+# ------------------------------------------------------------------------------------------ rope
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("tokens", [1301, 4099, 20001])
+@pytest.mark.parametrize("width,part", [(64, 64), (64, 32), (80, 40), (80, 20), (33, 6), (256, 128)])
+def test_rope_of_several_tokens_a_block(dtype, interleaved, tokens, width, part):
+    """From 1184 tokens on a block has several, the last one fewer: units of 8, 4, 2 and 1 pairs, heads that turn in part."""
+    g = gen(tokens + width)
+    heads, kv = (3, 1) if tokens < 20000 else (1, 1)
+    q, k = randn(g, tokens, heads, width, dtype=dtype), randn(g, tokens, kv, width, dtype=dtype)
+    pos = torch.randint(0, 100000, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    table = mrf.rope_table(part)
+    f, mul = block_ref.rope_frequencies(part)
+    got = mrf.rope(q, k, pos, table, interleaved)
+    alone, _ = mrf.rope(k, None, pos, table, interleaved)
+    assert torch.equal(alone, got[1])
+    for x, y in zip((q, k), got):
+        ref, size = block_ref.rope(x, pos, f, mul, interleaved)
+        within(y, ref, block_ref.rope_slack(size) + block_ref.half_step(dtype) * ref.abs() * 1.01 + (size > 0) * 2.0**-25)
+    mrf.rope(q, k, pos, table, interleaved, q_out=q, k_out=k)
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+
+
+# ------------------------------------------------------------------------------------------ norm
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", [(10001, 64), (9601, 200), (10001, 384), (10001, 520), (200, 8200), (331, 16384), (10001, 2049), (40001, 131),
+                                      (1500, 4096), (600, 16383)])
+def test_norm_of_several_rows_a_team(dtype, rows, dim):
+    """More rows than the launch has warps or blocks, so that each takes several: every kernel, plain and 8-bit."""
+    g = gen(rows + dim)
+    x, res, w = randn(g, rows, dim, dtype=dtype), randn(g, rows, dim, dtype=dtype), 1 + 0.1 * randn(g, dim)
+    for residual in (None, res):
+        y, h = block_ref.rms_norm(x, w, 1e-6, residual)
+        r = mrf.rms_norm(x, w, 1e-6, residual)
+        within(r.out, y, y.abs() * (block_ref.norm_slack(dim) + block_ref.half_step(dtype)) + 2.0**-25, "out")
+        if residual is not None:
+            within(r.residual, h, h.abs() * (block_ref.U32 + block_ref.half_step(dtype)) * 1.001 + 2.0**-25, "h")
+        for group in (0, 128):
+            q = mrf.rms_norm(x, w, 1e-6, residual, out_dtype=E4M3, group=group)
+            check_quant(q, y, group, dim)
+            if residual is not None:
+                assert torch.equal(q.residual, r.residual)
+
+
+# ------------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("dtype,width", [(F16, 64), (BF16, 128), (F32, 64), (F16, 36)])
+@pytest.mark.parametrize("cache", [0, 9000])
+def test_attention_wrong_offsets_write_no_other_rows(dtype, width, cache):
+    """Offsets beyond the tensors or descending: rows of the output that no clamped span holds, and what lies before and
+    behind it, stay as they were, on both kernels, with and without ranges of keys."""
+    g = gen(width)
+    q_rows = 12 if cache else 300
+    heads, kv = (8, 1) if cache else (4, 2)
+    k_rows = cache or q_rows
+    q, k, v = randn(g, q_rows, heads, width, dtype=dtype), randn(g, k_rows, kv, width, dtype=dtype), randn(g, k_rows, kv, width, dtype=dtype)
+    i32 = lambda t: torch.tensor(t, device="cuda", dtype=torch.int32)
+    big = 2**31 - 1
+    for off in ([0, 5], [-5, 4], [0, 1000], [10, 5], [big, big], [9, 3, 11], [2, 2, 2], [7, big, 3], [-big, -1, 6], [3, 8, 8, big]):
+        seqs = len(off) - 1
+        spans = [(min(max(a, 0), q_rows), min(max(b, 0), q_rows)) for a, b in zip(off, off[1:])]
+        lengths = [(None, None)] if not cache else [([3] * seqs, [cache - 10] * seqs), ([-9] * seqs, [1 << 30] * seqs), ([1 << 30] * seqs, [5] * seqs),
+                                                   ([7] * seqs, [-4] * seqs)]
+        for start, length in lengths:
+            pad = 40
+            whole = torch.full((q_rows + 2 * pad, heads, width), 7.0, device="cuda", dtype=dtype)
+            out = whole[pad : pad + q_rows]
+            mrf.attention_packed(q, k, v, i32(off), start and i32(start), length and i32(length), out=out)
+            mrf.ops_sync_status()
+            inside = torch.zeros(q_rows, dtype=torch.bool, device="cuda")
+            for a, b in spans:
+                inside[a:b] = True
+            assert (whole[:pad] == 7).all() and (whole[pad + q_rows :] == 7).all() and (out[~inside] == 7).all(), (off, start, length)
+
+
+FIRST = """
+import torch
+from axial_band_split_b200 import mrf
+torch.manual_seed(0)
+x = torch.randn(700, 8, 128, device="cuda", dtype=torch.float16)
+k, v = x[:, :2].contiguous(), x[:, 2:4].contiguous()
+wide = torch.randn(50, 4, 200, device="cuda", dtype=torch.float16)
+i32 = lambda *t: torch.tensor(t, device="cuda", dtype=torch.int32)
+off, off1, one, start, length, offw = i32(0, 300, 700), i32(0, 1), x[:1].contiguous(), i32(0), i32(700), i32(0, 50)
+pos, table = torch.arange(700, device="cuda"), mrf.rope_table(128)
+w = torch.ones(1024, device="cuda")
+def step():
+    n = mrf.rms_norm(x.flatten(1), w, residual=x.flatten(1), out_dtype=torch.float8_e4m3fn, group=128)
+    odd = mrf.rms_norm(x.flatten(1)[:, :1001])
+    q, kk = mrf.rope(x, k, pos, table, interleaved=False)
+    a = mrf.attention_packed(q, kk, v, off)
+    b = mrf.attention_packed(one, kk, v, off1, start, length)
+    c = mrf.attention_packed(wide, wide, wide, offw)
+    return [n.out.float(), n.scales, n.residual, odd.out, q, kk, a, b, c]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+want = step()
+mrf.ops_sync_status()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("equal")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """No call of the process came before the capture: what a first call sets up is set up inside it."""
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stdout + r.stderr
