@@ -116,7 +116,8 @@ mrf_status mrf_rope_table(const mrf_rope_config *c, uint64_t *turns, float *scal
 mrf_status mrf_rope(const mrf_rope_args *a, void *stream) {
   if (!a) return op_fail(MRF_EINVAL, "mrf_rope: null arguments");
   if (!real_type(a->dtype)) return op_fail(MRF_EINVAL, "mrf_rope: dtype must be F32, F16 or BF16");
-  if (a->tokens < 0 || a->tokens > INT32_MAX || a->heads < 1 || a->heads > 65536 || a->kv_heads < 0 || a->kv_heads > 65536 || (a->k != nullptr) < (a->kv_heads > 0))
+  if (a->tokens < 0 || a->tokens > INT32_MAX || a->heads < 1 || a->heads > 65536 || a->kv_heads < 0 ||
+      a->kv_heads > 65536 || (a->tokens > 0 && a->kv_heads > 0 && !a->k))
     return op_fail(MRF_ESHAPE, "mrf_rope: tokens in [0, 2^31), heads >= 1 and kv_heads >= 0 (0 without k) required");
   if (a->width < 2 || a->width > 1024 || a->part < 2 || a->part > a->width || (a->part & 1))
     return op_fail(MRF_ESHAPE, "mrf_rope: width up to 1024 and an even part in [2, width] required");

@@ -40,6 +40,16 @@ def test_rope_of_several_tokens_a_block(dtype, interleaved, tokens, width, part)
     assert torch.equal(q, got[0]) and torch.equal(k, got[1])
 
 
+def test_rope_of_no_tokens():
+    """A step without new tokens, new outputs and in place: q and k of no rows, whose tensors have null pointers."""
+    x = torch.zeros(4, 8, 64, device="cuda", dtype=F16)
+    pos, table = torch.arange(4, device="cuda"), mrf.rope_table(64)
+    for q, k in ((x[:0, :6], x[:0, 6:]), (x[:0], None)):
+        a, b = mrf.rope(q, k, pos[:0], table)
+        assert a.shape == q.shape and (b is None if k is None else b.shape == k.shape)
+        assert mrf.rope(q, k, pos[:0], table, q_out=q, k_out=k)[0] is q
+
+
 # ------------------------------------------------------------------------------------------ norm
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,dim", [(10001, 64), (9601, 200), (10001, 384), (10001, 520), (200, 8200), (331, 16384), (10001, 2049), (40001, 131),
