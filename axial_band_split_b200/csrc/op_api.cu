@@ -88,27 +88,31 @@ mrf_status mrf_rope_table(const mrf_rope_config *c, uint64_t *turns, float *scal
   if (c->scaling != MRF_ROPE_NONE && (!(c->factor >= 1.0) || !std::isfinite(c->factor)))
     return op_fail(MRF_EINVAL, "mrf_rope_table: factor must be >= 1");
   if (c->scaling == MRF_ROPE_NTK && c->part == 2) return op_fail(MRF_EINVAL, "mrf_rope_table: NTK needs part > 2");
-  const double pi2 = 6.283185307179586476925287, n = c->part;
-  double theta = c->theta, lo = 0, hi = 0;
-  if (c->scaling == MRF_ROPE_NTK) theta *= std::pow(c->factor, n / (n - 2));
+  // Frequencies in long double (64 bits of fraction): a double's 53 would be off by 2^-56 of a turn a position.
+  // The border dimensions of YARN are whole numbers, which double gives as their definition's usual form does.
+  const long double pi2 = 6.283185307179586476925286766559005768L, n = c->part, factor = c->factor;
+  long double theta = c->theta;
+  double lo = 0, hi = 0;
+  if (c->scaling == MRF_ROPE_NTK) theta *= std::pow(factor, n / (n - 2));
   if (c->scaling == MRF_ROPE_YARN) {
     const double fast = c->beta_fast == 0 && c->beta_slow == 0 ? 32 : c->beta_fast;
     const double slow = c->beta_fast == 0 && c->beta_slow == 0 ? 1 : c->beta_slow;
     if (!(c->original >= 1.0) || !std::isfinite(c->original) || !(slow > 0) || !(fast > slow) || !std::isfinite(fast))
       return op_fail(MRF_EINVAL, "mrf_rope_table: original >= 1 and beta_fast > beta_slow > 0 required");
-    lo = std::fmax(std::floor(n * std::log(c->original / (fast * pi2)) / (2 * std::log(theta))), 0.0);
-    hi = std::fmin(std::ceil(n * std::log(c->original / (slow * pi2)) / (2 * std::log(theta))), n - 1);
+    auto dim = [&](double t) { return c->part * std::log(c->original / (t * (double)pi2)) / (2 * std::log(c->theta)); };
+    lo = std::fmax(std::floor(dim(fast)), 0.0);
+    hi = std::fmin(std::ceil(dim(slow)), c->part - 1.0);
   }
   *scale = 1.f;
   if (c->scaling == MRF_ROPE_YARN && c->factor > 1.0) *scale = (float)(0.1 * std::log(c->factor) + 1.0);
   for (int i = 0; i < c->part / 2; ++i) {
-    double f = std::pow(theta, -2.0 * i / n);
-    if (c->scaling == MRF_ROPE_LINEAR) f /= c->factor;
+    long double f = std::pow(theta, -2 * i / n);
+    if (c->scaling == MRF_ROPE_LINEAR) f /= factor;
     if (c->scaling == MRF_ROPE_YARN) {
-      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
-      f = f / c->factor * r + f * (1 - r);
+      const long double r = std::fmin(std::fmax((i - lo) / (long double)std::fmax(hi - lo, 0.001), 0.0L), 1.0L);
+      f = f / factor * r + f * (1 - r);
     }
-    turns[i] = (uint64_t)std::llround(std::ldexp(f / pi2, 62)) << 2;  // f <= 1 radian: below 2^62 * 0.16
+    turns[i] = (uint64_t)std::llround(std::ldexp(f / pi2, 64));  // f <= 1 radian: below 2^64 * 0.16
   }
   return MRF_OK;
 }

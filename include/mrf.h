@@ -392,9 +392,10 @@ mrf_status mrf_rms_norm(const mrf_rms_norm_args *a, void *stream);
  *                    d(beta_fast), 0), hi = min(ceil d(beta_slow), part - 1) and r_i = (i - lo) /
  *                    max(hi - lo, 0.001) held to [0, 1]: f_i (1 - r_i) + f_i / factor * r_i, and
  *                    cos and sin times 0.1 ln(factor) + 1 (factor > 1).
- * turns[i] (part / 2 values, host) receives f_i / (2 pi) as a 64-bit binary fraction of a turn:
- * position * turns[i] modulo 2^64 is the angle's fraction of a turn with no error that grows into
- * the result at any position below 2^40.  *scale receives the factor on cos and sin.
+ * turns[i] (part / 2 values, host) receives f_i / (2 pi) as a 64-bit binary fraction of a turn, within
+ * 2^-63 of a turn: position * turns[i] modulo 2^64 is the angle's fraction of a turn, off by at most
+ * position * 2^-63.  That stays below fp32's own rounding of the angle (2^-26 of a turn) up to
+ * positions of 2^37.  *scale receives the factor on cos and sin.
  */
 typedef enum { MRF_ROPE_NONE = 0, MRF_ROPE_LINEAR = 1, MRF_ROPE_NTK = 2, MRF_ROPE_YARN = 3 } mrf_rope_scaling;
 typedef struct {

@@ -40,6 +40,26 @@ def test_rope_of_several_tokens_a_block(dtype, interleaved, tokens, width, part)
     assert torch.equal(q, got[0]) and torch.equal(k, got[1])
 
 
+def test_rope_far_positions_against_fifty_digits():
+    """Angles at positions up to 2^37 from frequencies that are not the table's: off by position * 2^-63 of a turn at most."""
+    from decimal import Decimal, localcontext
+    from test_block_ops_edges import PI, exact_turns
+    g = gen(12)
+    places = [0, 1, 4097, (1 << 20) + 3, (1 << 31) - 1, 1 << 31, (1 << 36) + 12345, (1 << 37) - 1, -(1 << 33), -(1 << 37)]
+    q = randn(g, len(places), 2, 128)
+    with localcontext() as ctx:
+        ctx.prec = 50
+        fractions = [[p * f % 1 for f in exact_turns(128, 10000.0)] for p in map(Decimal, places)]
+        angle = torch.tensor([[float(2 * PI * t) for t in row] for row in fractions], dtype=torch.float64, device="cuda")[:, None]
+    far = torch.tensor([abs(p) for p in places], dtype=torch.float64, device="cuda")[:, None, None] * 2.0**-63 * 6.2832
+    got, _ = mrf.rope(q, None, torch.tensor(places, device="cuda"), mrf.rope_table(128, 10000.0), interleaved=False)
+    a, b = q[..., :64].double(), q[..., 64:].double()
+    size = a.abs() + b.abs()
+    bound = block_ref.rope_slack(size) + size * far
+    within(got[..., :64], a * angle.cos() - b * angle.sin(), bound)
+    within(got[..., 64:], b * angle.cos() + a * angle.sin(), bound)
+
+
 def test_rope_of_no_tokens():
     """A step without new tokens, new outputs and in place: q and k of no rows, whose tensors have null pointers."""
     x = torch.zeros(4, 8, 64, device="cuda", dtype=F16)
