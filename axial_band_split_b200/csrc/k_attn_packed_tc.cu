@@ -71,6 +71,11 @@ constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsIo = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * kRegsLaunch, "register split over budget");
 constexpr float kRescaleLog2 = 8.f;  // a row's maximum is raised only when exceeded by more than 2^8
+// Probabilities and their sum carry a factor of 2^kUp.  fp16 ends at 2^-24: without the factor weights below 2^-14 of the
+// maximum would lose bits and those below 2^-25 vanish from the product while the sum has them, 2^-9 of the output with
+// 65536 such keys beside one that takes the weight.  2^7 is what 2^8 above the maximum leaves below 65504.
+template <bool kBF>
+constexpr float kUp = kBF ? 0.f : 7.f;
 // Key blocks of an item that are still to be loaded when the next one is taken: late, so that the longest items, which
 // come first, do not also get the first of the rest (a prompt of 4096 tokens, 16 heads: 69 us, 86 when it is taken at
 // once), and early enough for the time that taking one needs.
@@ -675,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const bool any_need = __any_sync(0xffffffffu, need);
-        // p = 2^(c s - c m), rounded to the type's pairs for the second product; l sums them unrounded
-        const float negm = m == -INFINITY ? 0.f : -m * c;
+        // p = 2^(c s - c m + kUp), rounded to the type's pairs for the second product; l sums them unrounded
+        const float negm = m == -INFINITY ? 0.f : fmaf(-m, c, kUp<kBF>);
         float2 sum[2] = {};
         uint32_t pk[kHalf / 2];
         exponentials<kBF, 0, kHalf>(sv, c, negm, sum, pk);
@@ -781,9 +786,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (row) {
         if (it.partial)
-          a.part_lse[((long long)it.u[t].split * a.q_rows + at) * a.heads + h] = l > 0.f || l != l ? m * c + log2f(l) : -INFINITY;
+          a.part_lse[((long long)it.u[t].split * a.q_rows + at) * a.heads + h] = l > 0.f || l != l ? m * c + (log2f(l) - kUp<kBF>) : -INFINITY;
         else if (a.lse)
-          a.lse[at * a.heads + h] = l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
+          a.lse[at * a.heads + h] = l > 0.f || l != l ? m * a.scale + logf(l * exp2f(-kUp<kBF>)) : -INFINITY;
       }
     }
   }

@@ -441,8 +441,9 @@ mrf_status mrf_rope(const mrf_rope_args *a, void *stream);
  * the keys up to i + n_k - n_q, so the same call serves a prompt, a prompt's next piece over a
  * cache, and one new token.  A query that sees no key gets out 0 and lse -inf.  lse (NULL: not
  * stored) is ln sum exp(scale q k) in natural units.  Scores, softmax statistics and sums are
- * fp32; the probabilities are rounded to the tensors' type for the second product (in fp32 for
- * F32), the output once.  Key rows outside a sequence are never used, whatever they hold; inside it
+ * fp32.  On the tensor cores the probabilities are rounded to the tensors' type for the second product
+ * (relative half steps; F16 weights below 2^-21 of the row's largest to multiples of 2^-31 of it), on
+ * the CUDA cores they stay fp32; the output is rounded once.  Key rows outside a sequence are never used, whatever they hold; inside it
  * keys masked by causality may be anything, but their values must be finite.  Rows
  * of out and lse that belong to no sequence are left as they were.  Offsets are read on the
  * device and held to the tensors' rows, so wrong ones give wrong rows but no access outside.

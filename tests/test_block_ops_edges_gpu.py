@@ -121,6 +121,34 @@ def test_attention_wrong_offsets_write_no_other_rows(dtype, width, cache):
             assert (whole[:pad] == 7).all() and (whole[pad + q_rows :] == 7).all() and (out[~inside] == 7).all(), (off, start, length)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("width", [64, 128])
+@pytest.mark.parametrize("queries,heads,kv", [(1, 8, 1), (300, 2, 1)])
+def test_attention_of_many_small_weights(dtype, width, queries, heads, kv):
+    """A key in every 1500 takes the weight and has no value; the others have 2^-24.5 to 2^-26.5 of it each, and all of the
+    output.  Beside the relative half steps a weight may be off by 2^-32 of the largest, half a step of fp16's smallest
+    numbers with the factor of 2^7; unscaled ones would lose most of the output."""
+    g = gen(width)
+    keys = 20000
+    x = 24.5 + 2 * torch.rand(keys, generator=g, device="cuda")
+    x[::1500] = 0
+    q = torch.zeros(queries, heads, width, device="cuda", dtype=dtype)
+    q[..., 0] = 1
+    k = torch.zeros(keys, kv, width, device="cuda", dtype=dtype)
+    k[..., 0] = (-x * 0.6931471805599453)[:, None].to(dtype)
+    v = (0.5 + torch.rand(keys, kv, width, generator=g, device="cuda")).to(dtype)
+    v[::1500] = 0
+    i32 = lambda *t: torch.tensor(t, device="cuda", dtype=torch.int32)
+    out, lse = mrf.attention_packed(q, k, v, i32(0, queries), i32(0), i32(keys), keys, causal=False, scale=1.0, return_lse=True)
+    ref, rlse, size, big = block_ref.attention(q, k, v, [(0, queries, 0, keys)], False, 1.0)
+    bound, lbound = block_ref.attention_slack(dtype, ref, size, big, keys, width)
+    share = keys * 2.0**-32 / rlse.exp()[..., None] * 1.5  # (values up to 1.5)
+    # the output itself is a small number of its type
+    step = 2.0**-25 if dtype == F16 else 0.0
+    within(out, ref, bound + share + step)
+    within(lse, rlse, lbound)
+
+
 FIRST = """
 import torch
 from axial_band_split_b200 import mrf
