@@ -28,9 +28,10 @@
 // exponentials.  With wider v S_t at 128 t and O_t at 256 + 128 t fill it.  P is handed over in two
 // halves of 64 keys, so P V of the first runs under the second's exponentials; with wider v the first
 // half overwrites S_t (the softmax has read it all), the second goes through shared memory, and the
-// issuer queues the next block's scores right behind the first half's P V, which the tensor core runs in
-// order: they are ready when the second half's exponentials are done.  (With both halves over S_t they
-// had to wait for the whole P V, about 1200 of a block's 4000 clk.)
+// issuer queues the next block's scores as soon as the first half's P V has ended: they are ready when the
+// second half's exponentials are done.  (With both halves over S_t they had to wait for the whole P V,
+// about 1200 of a block's 4000 clk.  Queued right behind the first half, without a wait, they were no
+// faster: a prompt of 16384 tokens 841 us against 832, token steps 105 against 107.)
 //
 // K and V blocks stream through one ring in the order of their use (separate keys: the two units'
 // streams take turns).  Both issuers acknowledge every slot, their own when its reads have ended and
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *item_full = bars + 16, *item_empty = bars + 20;  // [kItems]
   uint64_t *done = bars + 24, *block_full = bars + 25;
   uint64_t *kv_full = bars + 26, *kv_empty = kv_full + C::slots;
-  static_assert(26 + 2 * C::slots <= 62, "barrier area");
+  uint64_t *half_done = bars + 60;                       // [2]: the first half's P V has ended (with P over S)
+  static_assert(26 + 2 * C::slots <= 60, "barrier area");
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 62);
   volatile int *abort = reinterpret_cast<int *>(bars + 63);
   Item *items = reinterpret_cast<Item *>(smem + C::item);
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(p_full + 2 * t, C::warps);
       tc::mbar_init(p_full + 2 * t + 1, C::warps);
       tc::mbar_init(pv_done + t, 1);
+      tc::mbar_init(half_done + t, 1);
       tc::mbar_init(o_free + t, C::warps);
     }
     for (int i = 0; i < kItems; ++i) { tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 3 + 2 * C::warps); }
@@ -503,6 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tP = C::overlay ? tS : tmem + 384 + 64 * t;
       int ring = 0, qn = 0;             // next ring slot, q buffer
       uint32_t ring_phase = 0, q_phase = 0, units = 0, blocks = 0;  // parities: of those, and of this unit's
+      uint32_t half_phase = 0;
+      bool half_open = false;  // a P V that reads P over S was queued and not waited for
       const uint64_t p_desc = tc::sw128_kmajor_desc(tc::smem_u32(smem + C::p) + (kFew ? 0 : t * C::tile));
       // operand descriptors at the first byte of their areas: an offset adds to the address field (bytes
       // / 16, below 2^14 within shared memory)
@@ -546,8 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance();
           return sl;
         };
-        // scores of block j (with wide v over the half of P that P V, queued before, reads)
+        // scores of block j.  With wide v they overwrite the half of P that the P V queued before reads: matrix
+        // instructions of one thread are only promised to run in order where they share an accumulator, so that P V is
+        // waited for (its 64 keys, while the softmax works on the second half).
         auto issue_s = [&](int j, int sl) {
+          if (half_open) {
+            if (!tc::mbar_wait(half_done + t, half_phase, status, 65, abort)) return false;
+            half_phase ^= 1;
+            half_open = false;
+          }
           tc::tc_fence_after();
           const uint32_t id = klen - j * kKeys > kHalf ? id_s : id_s64;
           const uint64_t qd = q_desc + ((qn * C::qbuf) >> 4), kd = k_desc + ((sl * C::slot) >> 4);
@@ -559,21 +571,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit(leader, s_full + t);
           commit(leader, kv_empty + sl);
           if (j == nb - 1) commit(leader, q_empty + qn);
+          return true;
         };
         if (!tc::mbar_wait(q_full + qn, q_phase, status, 55, abort)) { ok = false; break; }
         if (nb == 0 && lane == 0) tc::mbar_arrive(q_empty + qn);
         if (nb > 0) {
           const int sk = take(k_elem<C::overlay>(0));
           // (S_t was read by the previous unit's last softmax: its P V has been queued)
-          if (sk < 0) { ok = false; break; }
-          issue_s(0, sk);
+          if (sk < 0 || !issue_s(0, sk)) { ok = false; break; }
         }
         for (int j = 0; j < nb; ++j) {
           int sk = 0, sl = 0;
           if (!C::overlay && j + 1 < nb) {
             sk = take(k_elem<false>(j + 1));
-            if (sk < 0 || !tc::mbar_wait(s_free + t, blocks, status, 57, abort)) { ok = false; break; }
-            issue_s(j + 1, sk);
+            if (sk < 0 || !tc::mbar_wait(s_free + t, blocks, status, 57, abort) || !issue_s(j + 1, sk)) { ok = false; break; }
           }
           sl = take(v_elem<C::overlay>(j, all));
           if (C::overlay && sl >= 0 && j + 1 < nb) sk = take(k_elem<true>(j + 1));  // ahead of the wait for P
@@ -600,7 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps) mma_ts(leader, tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), id_pv, j != 0 || kk != 0);
-          if (C::overlay && j + 1 < nb) issue_s(j + 1, sk);
+          if (C::overlay) {
+            commit(leader, half_done + t);
+            half_open = true;
+            if (j + 1 < nb && !issue_s(j + 1, sk)) { ok = false; break; }
+          }
           if (!tc::mbar_wait(p_full + 2 * t + 1, blocks, status, 58, abort)) { ok = false; break; }
           tc::tc_fence_after();
 #pragma unroll
