@@ -242,6 +242,7 @@ class _Torch:
                                                             torch.uint8)
         self.empty_like = torch.empty_like  # keeps the order of the strides, so that is where outputs' strides come from
         self.grad, self.device, self.Tensor = torch.is_grad_enabled, torch.cuda.current_device, torch.Tensor
+        self.forward = torch.autograd.forward_ad
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -266,9 +267,15 @@ def _code(t, x, name, dev=None):
     at = x.get_device()
     if at < 0 or (dev is not None and at != dev):
         raise MrfError(-1, f"{name} must be on {'a CUDA device' if dev is None else f'cuda:{dev}'}, is on {x.device}")
-    if x.requires_grad and t.grad():
-        raise MrfError(-1, f"{name} requires a gradient; the library is for inference")
+    if (x.requires_grad and t.grad()) or getattr(t.forward, "_current_level", 0) >= 0:
+        _no_gradient(t, x, name)
     return code
+
+
+def _no_gradient(t, x, name):
+    """Refuses what a gradient or, within a level of forward-mode derivatives, a tangent would be lost of."""
+    if (x.requires_grad and t.grad()) or t.forward.unpack_dual(x).tangent is not None:
+        raise MrfError(-1, f"{name} requires a gradient; the library is for inference")
 
 
 def _like(t, x, dtype, dev, shape, name):
@@ -280,8 +287,8 @@ def _like(t, x, dtype, dev, shape, name):
     st = x.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise MrfError(-1, f"{name}: the last dimension must be contiguous")
-    if x.requires_grad and t.grad():
-        raise MrfError(-1, f"{name} requires a gradient; the library is for inference")
+    if (x.requires_grad and t.grad()) or getattr(t.forward, "_current_level", 0) >= 0:
+        _no_gradient(t, x, name)
     return st
 
 

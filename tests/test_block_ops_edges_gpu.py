@@ -149,6 +149,24 @@ def test_attention_of_many_small_weights(dtype, width, queries, heads, kv):
     within(lse, rlse, lbound)
 
 
+# ------------------------------------------------------------------------------------- refusals
+def test_tangents_are_refused():
+    """Forward-mode derivatives: a tensor with a tangent is refused as one that requires a gradient, the others are not."""
+    import torch.autograd.forward_ad as forward_ad
+    x = torch.ones(4, 2, 64, device="cuda", dtype=F16)
+    off, pos, table = torch.tensor([0, 4], device="cuda", dtype=torch.int32), torch.arange(4, device="cuda"), mrf.rope_table(64)
+    w = torch.ones(64, device="cuda")
+    with forward_ad.dual_level():
+        d, dw = forward_ad.make_dual(x, torch.ones_like(x)), forward_ad.make_dual(w, torch.ones_like(w))
+        for call in (lambda: mrf.rms_norm(d), lambda: mrf.rms_norm(x, dw), lambda: mrf.rms_norm(x, residual=d), lambda: mrf.rope(d, None, pos, table),
+                     lambda: mrf.rope(x, d, pos, table), lambda: mrf.attention_packed(d, x, x, off), lambda: mrf.attention_packed(x, d, x, off),
+                     lambda: mrf.attention_packed(x, x, d, off)):
+            with pytest.raises(mrf.MrfError, match="gradient"):
+                call()
+        assert mrf.rms_norm(x, w, residual=x).out.shape == x.shape and mrf.attention_packed(x, x, x, off).shape == x.shape
+        assert mrf.rope(x, x, pos, table)[1].shape == x.shape
+
+
 FIRST = """
 import torch
 from axial_band_split_b200 import mrf
