@@ -468,14 +468,17 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
     elif k_out is not None:
         raise MrfError(-1, "k_out without k")
     _vector(t, positions, dev, tokens, "positions", wide=True)
-    if not isinstance(table, RopeTable) or table.turns.get_device() != dev:
+    turns = table.turns if isinstance(table, RopeTable) else None
+    if not isinstance(turns, t.Tensor) or turns.get_device() != dev or turns.dtype != t.i64:
         raise MrfError(-1, f"table must come from rope_table on cuda:{dev}")
+    if turns.dim() != 1 or 2 * turns.shape[0] != table.part or (table.part > 2 and turns.stride(0) != 1):
+        raise MrfError(-2, f"table must have a contiguous value for each of its {table.part} / 2 pairs, has {tuple(turns.shape)}")
     if q_out is None:
         q_out, qos = _new_like(t, q)
     else:
         qos = _like(t, q_out, dtype, dev, shape, "q_out")
     status = (_lib or lib()).mrf_rope(_ROPE.pack(
-        q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(), table.turns.data_ptr(), tokens, qs[0], qs[1],
+        q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(), turns.data_ptr(), tokens, qs[0], qs[1],
         ks[0], ks[1], qos[0], qos[1], kos[0], kos[1], heads, kv_heads, width, table.part, code, positions.dtype is t.i64,
         bool(interleaved), table.scale), t.stream(dev))
     if status:
