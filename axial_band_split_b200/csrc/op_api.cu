@@ -195,7 +195,9 @@ mrf_status mrf_attention(const mrf_attention_args *a, void *stream) {
     return op_fail(MRF_EINVAL, "mrf_attention: the workspace must hold %zu bytes, 16-byte aligned", need);
   cudaError_t e = cudaSuccess;
   if (tc && launch_attention_packed_tc(*a, st, &e)) return op_done(e, "mrf_attention");
-  return op_done(launch_attention_rows(*a, st), "mrf_attention");
+  mrf_attention_args rest = *a;
+  if (tc) rest.workspace_bytes = need;  // what was checked, for a kernel that would like more
+  return op_done(launch_attention_rows(rest, st), "mrf_attention");
 }
 
 mrf_status mrf_ops_sync_status(void *stream) {

@@ -179,6 +179,28 @@ def test_rotary_tables_that_do_not_hold_their_pairs_are_refused():
     assert torch.equal(part[..., 32:], x[..., 32:])
 
 
+def test_attention_without_a_tensor_map_uses_no_unchecked_workspace():
+    """A token stride that no tensor map takes (the row behind it is of no sequence): the CUDA cores compute, and a null
+    workspace is not written although workspace_bytes names some, because the call needs none."""
+    import ctypes
+    from test_block_ops import attention_args
+    g = gen(3)
+    q, k, v = randn(g, 2, 64, 128, dtype=F16), randn(g, 384, 1, 128, dtype=F16), randn(g, 384, 1, 128, dtype=F16)
+    i32 = lambda *t: torch.tensor(t, device="cuda", dtype=torch.int32)
+    out, off, start, length = torch.full_like(q, 7.0), i32(0, 1), i32(0), i32(384)
+    a = attention_args(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), out=out.data_ptr(), q_offsets=off.data_ptr(), k_start=start.data_ptr(),
+                       k_len=length.data_ptr(), workspace=None, workspace_bytes=1 << 40, q_rows=2, k_rows=384, q_token_stride=1 << 41, q_head_stride=128,
+                       k_token_stride=128, k_head_stride=128, v_token_stride=128, v_head_stride=128, out_token_stride=64 * 128, out_head_stride=128,
+                       seqs=1, heads=64, kv_heads=1, width=128, v_width=128, scale=128**-0.5)
+    need = ctypes.c_size_t(1)
+    assert mrf.lib().mrf_attention_workspace(ctypes.byref(a), ctypes.byref(need)) == 0 and need.value == 0
+    assert mrf.lib().mrf_attention(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    ref, _, size, big = block_ref.attention(q, k, v, [(0, 1, 0, 384)], True, 128**-0.5)
+    bound, _ = block_ref.attention_slack(F16, ref, size, big, 384, 128)
+    within(out[:1], ref[:1], bound[:1] + 2.0**-25)
+    assert (out[1:] == 7).all()
+
+
 FIRST = """
 import torch
 from axial_band_split_b200 import mrf
