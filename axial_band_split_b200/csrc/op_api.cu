@@ -5,6 +5,7 @@
 #include <cstdio>
 
 #include "block_ops.h"
+#include "op_status.h"
 
 using namespace mrf;
 
@@ -201,10 +202,17 @@ mrf_status mrf_attention(const mrf_attention_args *a, void *stream) {
 }
 
 mrf_status mrf_ops_sync_status(void *stream) {
+  static ExpiredWaits waits[64];
+  static thread_local unsigned seen[64] = {};
+  int dev = 0;
   unsigned word[2] = {0, 0};
-  const mrf_status s = op_done(attention_tc_status(word, static_cast<cudaStream_t>(stream)), "mrf_ops_sync_status");
-  if (s != MRF_OK || word[0] == 0) return s;
-  return op_fail(MRF_ETIMEOUT, "mrf_attention: a bounded wait expired on the device (site %u)", word[1]);
+  mrf_status s = op_done(cudaGetDevice(&dev), "mrf_ops_sync_status");
+  if (s == MRF_OK) s = op_done(attention_tc_status(word, static_cast<cudaStream_t>(stream)), "mrf_ops_sync_status");
+  if (s != MRF_OK) return s;
+  ExpiredWaits &w = waits[dev % 64];
+  if (word[0] != 0) w.found(word[1]);
+  if (!w.since(seen[dev % 64])) return MRF_OK;
+  return op_fail(MRF_ETIMEOUT, "mrf_attention: a bounded wait expired on the device (site %u)", w.site.load());
 }
 
 }  // extern "C"

@@ -554,7 +554,8 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
 
 
 def ops_sync_status(stream=None):
-    """mrf_ops_sync_status: wait for `stream` and raise if a block operator's kernel gave up a wait."""
+    """mrf_ops_sync_status: wait for `stream` and raise if a block operator's kernel on the current device gave up a wait
+    since this thread last asked (nothing else reports it)."""
     _check(lib().mrf_ops_sync_status(_stream_ptr(stream)))
 
 

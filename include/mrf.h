@@ -480,7 +480,9 @@ mrf_status mrf_attention(const mrf_attention_args *a, void *stream);
 /*
  * mrf_ops_sync_status - wait for `stream`, then report the block operators' status on the current
  * device as mrf_sync_status does for a handle: MRF_OK, MRF_ETIMEOUT if a kernel's bounded wait
- * expired since the last call (the word is cleared), or MRF_ECUDA.
+ * expired there since the calling thread last asked (or, at its first call, since the library was
+ * loaded), or MRF_ECUDA.  The status is the device's, whatever the stream: a thread also learns of
+ * the calls of others.  Nothing else reports it: mrf_attention has returned when its kernels run.
  */
 mrf_status mrf_ops_sync_status(void *stream);
 

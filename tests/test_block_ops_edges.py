@@ -1,6 +1,8 @@
 """The block operators' smallest calls and their tables against arithmetic that is not theirs (no GPU)."""
 import ctypes
 import math
+import os
+import subprocess
 from decimal import Decimal, localcontext
 
 import numpy as np
@@ -50,3 +52,39 @@ def test_rope_table_against_fifty_digits(part, theta, scaling, factor, original)
         ctx.prec = 50
         for t, want in zip(got.tolist(), exact_turns(part, theta, scaling, factor, original)):
             assert abs(Decimal(t) - want * 2**64) <= 2
+
+
+STATUS = r"""
+#include <cassert>
+#include <thread>
+#include "op_status.h"
+int main() {
+  mrf::ExpiredWaits w;
+  unsigned a = 0, b = 0;
+  assert(!w.since(a) && !w.since(b));
+  w.found(61);  // one thread read the device's word and cleared it
+  assert(w.since(a) && !w.since(a));
+  assert(w.since(b) && w.site.load() == 61 && !w.since(b));  // the other learns of it all the same, once
+  w.found(53);
+  w.found(54);
+  assert(w.since(b) && !w.since(b) && w.since(a));
+  unsigned told[4] = {};
+  std::thread t[4];
+  for (int i = 0; i < 4; ++i)
+    t[i] = std::thread([&, i] {
+      unsigned seen = 0;
+      if (i == 0) w.found(7);
+      while (!told[i]) told[i] = w.since(seen);
+    });
+  for (auto &x : t) x.join();
+  return told[0] + told[1] + told[2] + told[3] == 4 ? 0 : 1;
+}
+"""
+
+
+def test_an_expired_wait_is_told_to_every_thread(tmp_path):
+    """The device's word is cleared by the first thread that asks: the others must not lose the answer."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "axial_band_split_b200", "csrc")
+    (tmp_path / "status.cpp").write_text(STATUS)
+    subprocess.run(["g++", "-std=c++17", "-pthread", "-I" + csrc, "-o", str(tmp_path / "status"), str(tmp_path / "status.cpp")], check=True)
+    assert subprocess.run([str(tmp_path / "status")], timeout=60).returncode == 0
