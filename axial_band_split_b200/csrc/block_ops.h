@@ -38,6 +38,9 @@ __device__ __forceinline__ float load_any(const void *p, int dtype, long long i)
   return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
+// The current device's SMs, asked once a device (k_attn_packed_tc.cu).
+int sm_count();
+
 // Each queues its kernels on st; the arguments have been checked (op_api.cu).
 cudaError_t launch_rms_norm(const mrf_rms_norm_args &a, cudaStream_t st);
 cudaError_t launch_rope(const mrf_rope_args &a, cudaStream_t st);

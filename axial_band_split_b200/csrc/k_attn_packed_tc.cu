@@ -911,19 +911,6 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   return cudaGetLastError();
 }
 
-int sm_count() {
-  static std::atomic<int> known[64];
-  const int dev = current_device();
-  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return 148;
-  }
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 // Sequences whose queries fill no more than 32 rows of a tile on average (single new tokens) take tiles of 32 (32 tokens
 // over 500 to 8191 keys 106 us against 145 with 128 rows, 64 over 2000 92 and 116; with a piece of 256 more among them
 // 116 and 117).
@@ -936,6 +923,19 @@ AttentionSplit split_of(const mrf_attention_args &a) { return attention_split(a,
 bool mult8(long long n, long long stride) { return n <= 1 || (stride > 0 && stride % 8 == 0); }
 
 }  // namespace
+
+int sm_count() {
+  static std::atomic<int> known[64];
+  const int dev = current_device();
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 bool attention_tc_takes(const mrf_attention_args &a) {
   if (a.dtype != MRF_DTYPE_F16 && a.dtype != MRF_DTYPE_BF16) return false;
@@ -1037,7 +1037,7 @@ bool launch_attention_packed_tc(const mrf_attention_args &m, cudaStream_t st, cu
   // many ranges: a block a row; few: a warp
   const bool wide = a.max_splits > 8;
   const long long rows = m.q_rows * m.heads;
-  cfg.gridDim = dim3((unsigned)std::min<long long>(wide ? rows : (rows + 3) / 4, 148 * 16));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(wide ? rows : (rows + 3) / 4, 16 * sm_count()));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

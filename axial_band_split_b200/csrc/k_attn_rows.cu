@@ -335,7 +335,7 @@ cudaError_t launch(const mrf_attention_args &a, const Tiles &g, cudaStream_t st)
   k<<<(unsigned)std::min<long long>(g.units, 1 << 30), 256, smem, st>>>(a, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || g.chunk == 0) return e;
-  rows_join_kernel<T><<<(unsigned)std::min<long long>((a.q_rows * a.heads + 3) / 4, 148 * 16), 128, 0, st>>>(a, g);
+  rows_join_kernel<T><<<(unsigned)std::min<long long>((a.q_rows * a.heads + 3) / 4, 16 * sm_count()), 128, 0, st>>>(a, g);
   return cudaGetLastError();
 }
 template <class T>

@@ -532,7 +532,7 @@ cudaError_t launch_stream(const mrf_rms_norm_args &a, const Plan &p, cudaStream_
   const int smem = kAhead * (kRes ? 2 : 1) * 2 * (int)sizeof(T) / 2 * 16 * 32 * warps;
   if (const cudaError_t e = allow_smem<rms_norm_stream_kernel<T, kMode, kRes>>()) return e;
   const int blocks = std::max(1, std::min(32 / warps, 220 * 1024 / (smem + 1280)));  // on an SM, at 64 registers a thread
-  k<<<(int)std::min<long long>(a.rows, 148 * blocks), 32 * warps, smem, st>>>(a, p);
+  k<<<(int)std::min<long long>(a.rows, sm_count() * blocks), 32 * warps, smem, st>>>(a, p);
   return cudaGetLastError();
 }
 
@@ -550,24 +550,25 @@ cudaError_t launch(const mrf_rms_norm_args &a, bool vec, cudaStream_t st) {
   p.inv_eps = std::min(1.f / a.eps, 3.4e38f);  // finite: a row of zeros stays zeros
   p.log2_group = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   const int chunks = (a.dim + 255) / 256;  // of 256 columns: a vector of each lane of a warp
-  const bool few = a.rows < 148 * 4;       // rows that do not fill the SMs
+  const int sms = sm_count();
+  const bool few = a.rows < sms * 4;       // rows that do not fill the SMs
   if (!vec) {
     // a warp a row up to 2048 columns where there are rows for every warp (20000 x 2001: 101 us against 153 with a block a row,
     // x 131: 13 and 52; but 16000 x 4097: 286 and 195, and 300 x 131: 4.0 and 2.9)
     if (chunks <= 8 && !few) {
       const int warps = 4, smem = warps * a.dim * (int)sizeof(float);
       if (const cudaError_t e = allow_smem<rms_norm_odd_kernel<T, true>>()) return e;
-      rms_norm_odd_kernel<T, true><<<(int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 64), 32 * warps, smem, st>>>(a, p);
+      rms_norm_odd_kernel<T, true><<<(int)std::min<long long>((a.rows + warps - 1) / warps, sms * 64), 32 * warps, smem, st>>>(a, p);
     } else {
       const int smem = a.dim * (int)sizeof(float);
       if (const cudaError_t e = allow_smem<rms_norm_odd_kernel<T, false>>()) return e;
-      rms_norm_odd_kernel<T, false><<<(int)std::min<long long>(a.rows, 148 * 64), 256, smem, st>>>(a, p);
+      rms_norm_odd_kernel<T, false><<<(int)std::min<long long>(a.rows, sms * 64), 256, smem, st>>>(a, p);
     }
   } else if (chunks == 1) {  // a warp a row (40000 x 64: 10.7 us against 14.5 with blocks; x 256: 15.5 and 15.3)
     const int warps = few ? 1 : 8;
-    const int grid = (int)std::min<long long>((a.rows + warps - 1) / warps, 148 * 64 / warps);
+    const int grid = (int)std::min<long long>((a.rows + warps - 1) / warps, sms * 64 / warps);
     rms_norm_kernel<T, 1, true><<<grid, 32 * warps, 0, st>>>(a, p);
-  } else if (chunks == 2 && !few && a.rows <= 148 * 64) {
+  } else if (chunks == 2 && !few && a.rows <= sms * 64) {
     // a warp a row while every row finds a warp at once (4201 x 384: 3.4 us against 4.9 streamed, x 512: 3.8 and
     // 5.0; 9472 x 384: 5.5 and 6.2; 40000 x 384: 24 and 20, so not there; 4201 x 1024: 6.3 and 5.5, nor there)
     rms_norm_kernel<T, 2, true><<<(int)((a.rows + 7) / 8), 256, 0, st>>>(a, p);
@@ -580,7 +581,7 @@ cudaError_t launch(const mrf_rms_norm_args &a, bool vec, cudaStream_t st) {
     if (a.residual) return mode == 0 ? launch_stream<T, 0, true>(a, p, st) : mode == 1 ? launch_stream<T, 1, true>(a, p, st) : launch_stream<T, 2, true>(a, p, st);
     return mode == 0 ? launch_stream<T, 0, false>(a, p, st) : mode == 1 ? launch_stream<T, 1, false>(a, p, st) : launch_stream<T, 2, false>(a, p, st);
   } else {
-    rms_norm_kernel<T, 5, false><<<(int)std::min<long long>(a.rows, 148), 32 * ((chunks + 4) / 5), 0, st>>>(a, p);
+    rms_norm_kernel<T, 5, false><<<(int)std::min<long long>(a.rows, sms), 32 * ((chunks + 4) / 5), 0, st>>>(a, p);
   }
   return cudaGetLastError();
 }

@@ -124,7 +124,7 @@ void launch(const mrf_rope_args &a, cudaStream_t st) {
   s.units = s.rot + (in_place ? 0 : (a.width - a.part + 2 * N - 1) / (2 * N));
   // about 1024 units a block, as long as there are blocks enough for every SM
   const long long per = (long long)(a.heads + a.kv_heads) * s.units;
-  long long t = std::max(1ll, std::min<long long>({1024 / per, a.tokens / (148 * 4), kMaxPairs / (a.part / 2)}));
+  long long t = std::max(1ll, std::min<long long>({1024 / per, a.tokens / (4 * sm_count()), kMaxPairs / (a.part / 2)}));
   s.tokens = (int)t;
   rope_kernel<T, N><<<(int)((a.tokens + t - 1) / t), kThreads, 0, st>>>(a, s);
 }
