@@ -469,9 +469,9 @@ def rope(q, k, positions, table, interleaved=True, q_out=None, k_out=None, strea
         raise MrfError(-1, "k_out without k")
     _vector(t, positions, dev, tokens, "positions", wide=True)
     turns = table.turns if isinstance(table, RopeTable) else None
-    if not isinstance(turns, t.Tensor) or turns.get_device() != dev or turns.dtype != t.i64:
+    if not isinstance(turns, t.Tensor) or turns.dtype != t.i64 or turns.get_device() != dev:
         raise MrfError(-1, f"table must come from rope_table on cuda:{dev}")
-    if turns.dim() != 1 or 2 * turns.shape[0] != table.part or (table.part > 2 and turns.stride(0) != 1):
+    if 2 * turns.numel() != table.part or not turns.is_contiguous():
         raise MrfError(-2, f"table must have a contiguous value for each of its {table.part} / 2 pairs, has {tuple(turns.shape)}")
     if q_out is None:
         q_out, qos = _new_like(t, q)

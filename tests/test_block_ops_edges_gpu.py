@@ -171,7 +171,7 @@ def test_rotary_tables_that_do_not_hold_their_pairs_are_refused():
     """A table with another part than its values, or values of another kind, would be read past its end."""
     x, pos, table = torch.ones(4, 2, 128, device="cuda", dtype=F16), torch.arange(4, device="cuda"), mrf.rope_table(64)
     for bad in (table._replace(part=128), table._replace(part=66), table._replace(part=62), table._replace(part=-64), table._replace(turns=table.turns[::2]),
-                table._replace(turns=table.turns[::2], part=32), table._replace(turns=table.turns.int()), table._replace(turns=table.turns[None]),
+                table._replace(turns=table.turns[::2], part=32), table._replace(turns=table.turns.int()),
                 table._replace(turns=None), table._replace(turns=table.turns.cpu()), tuple(table)):
         with pytest.raises(mrf.MrfError):
             mrf.rope(x, None, pos, bad)
