@@ -43,11 +43,11 @@
 // be NaN, are zeroed in shared memory before the second product.
 //
 // Measured, against a copy of 6.57 TB/s and a matrix product of 1669 TFLOP/s on the same device:
-//   a causal prompt of 16384 tokens, 16 heads of 128 over 4   0.86 ms, 1.28 PFLOP/s, 0.77
-//   7 causal prompts of 200 to 4096 tokens, 32 over 8         0.30 to 0.34 ms, 0.9 to 1.0 PFLOP/s, 0.54 to 0.6
+//   a causal prompt of 16384 tokens, 16 heads of 128 over 4   0.84 ms, 1.31 PFLOP/s, 0.78
+//   7 causal prompts of 200 to 4096 tokens, 32 over 8         0.29 to 0.34 ms, 0.9 to 1.03 PFLOP/s, 0.54 to 0.62
 //   8 x 1100 tokens both ways, 8 heads of 64                  44 to 47 us, 0.42 to 0.45 PFLOP/s
 //   a token of each of 32 sequences of 500 to 8191 keys       106 us, 5.0 TB/s, 0.76
-//   a token after 65536 keys                                  58 us, 4.6 TB/s, 0.70
+//   a token after 65536 keys                                  58.5 us, 4.6 TB/s, 0.70
 // A block of 128 keys costs both units together 3400 to 3700 clk, where its matrix instructions need 2800 with widths of
 // 128 and its exponentials, at 16 a clk and SM, 2048: each unit's row loads, maxima, conversions and stores stand beside its
 // exponentials.  With 64 those phases bound it, and an item's start and output (about 4000 clk each) weigh as much as a block

@@ -6,11 +6,13 @@
 // row's sum of squares and the maxima that the 8-bit scales need come from the same pass over the
 // registers, and one exchange between the warps serves both.
 //
-// Rows up to 256 wide take a warp each (no exchange between warps), wider ones a block.  Rows in 16-byte pieces
-// stream through rms_norm_stream_kernel, few, narrow or very wide ones go through rms_norm_kernel, and rows without
-// that alignment through rms_norm_odd_kernel.  The arithmetic, about 10 instructions a value with the conversions,
-// is the next bound: it runs on packed fp32 pairs, and the work that a row costs every thread (the sums' exchange,
-// the root, the scales) is spread over its 16 values.
+// Rows in 16-byte pieces: up to 256 columns, and up to 512 while every row finds a warp at once, take a warp each (no
+// exchange between warps), few rows of up to 2048 columns and all above 8192 a block each in the same
+// rms_norm_kernel; the others stream through rms_norm_stream_kernel.  Rows without that alignment go through
+// rms_norm_odd_kernel, many of up to 2048 columns with a warp each, else with a block.  launch() has the borders and
+// what both sides measured.  The arithmetic, about 10 instructions a value with the conversions, is the next bound:
+// it runs on packed fp32 pairs, and the work that a row costs every thread (the sums' exchange, the root, the scales)
+// is spread over its 16 values.
 // 16384 x 4096 bf16 with residual and an e4m3 output (472 MB): 87.5 us, 5.4 TB/s, 0.82 of the measured copy
 // (a first form with 64-bit index products and a division a value executed 40 instructions a value: 113 us).
 #include <cuda_fp8.h>
@@ -370,9 +372,9 @@ __global__ void __launch_bounds__(256, 4) rms_norm_odd_kernel(const mrf_rms_norm
   }
 }
 
-// Many rows of 513 to 8192 columns in 16-byte pieces: a block a row, two vectors a thread.  The loads of
-// kAhead rows are in flight at any time (asynchronous copies into shared memory, 48 KB a block at
-// 4096 columns of 16 bits), the weight stays in registers, and addresses advance by additions.
+// Rows of 257 to 8192 columns in 16-byte pieces, but for those that launch() finds faster elsewhere: a block a row,
+// two vectors a thread.  The loads of kAhead rows are in flight at any time (asynchronous copies into shared memory,
+// 48 KB a block at 4096 columns of 16 bits), the weight stays in registers, and addresses advance by additions.
 // kMode: 0 the output is T, 1 e4m3 with a scale a row, 2 with a scale a group.
 constexpr int kAhead = 3;
 

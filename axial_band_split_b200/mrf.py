@@ -10,7 +10,8 @@ there is no fallback path.
 
 The block operators (rms_norm, rope, attention_packed) take and return torch CUDA tensors and need
 no model: they are the steps between the matrix products of a transformer block over sequences of
-different lengths packed without padding.
+different lengths packed without padding.  With stream= a call's new tensors belong to that stream;
+tensors of another stream are the caller's to order before it and to keep until its work has run.
 """
 from __future__ import annotations
 
@@ -494,7 +495,8 @@ def attention_packed(q, k, v, q_offsets, k_start=None, k_len=None, max_k=0, caus
     bfloat16 or float32 with any token and head strides.  Sequence b owns the query rows q_offsets[b] ..
     q_offsets[b + 1] (int32 [seqs + 1]) and the key rows k_start[b] .. k_start[b] + k_len[b] (int32 [seqs];
     without them its query rows).  causal: the last query sees all keys of its sequence.  max_k: an upper
-    bound of the key counts known on the host (0: k's rows), which only decides how the work is split.
+    bound of the key counts known on the host (0: k's rows), which only decides how the work is split: new
+    tokens over long caches are the faster the closer it is.
     Rows of no sequence keep what `out` held (a new `out` is uninitialised there).  Returns out
     [q_rows, heads, v_width], or (out, lse float32 [q_rows, heads]) with return_lse."""
     t = _torch or _t()

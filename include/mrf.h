@@ -342,7 +342,8 @@ int mrf_launches_per_forward(const mrf_handle *h, int B, int T);
  * Every pointer below is a device pointer on the current device unless it says host; the work is
  * queued on `stream`, nothing is allocated, nothing waits, and every call may be captured into a
  * CUDA graph (pointers and sizes are then those of the capture; offsets, lengths and positions
- * are read from device memory when the work runs).  Strides count elements; the innermost
+ * are read from device memory when the work runs).  What a call is given must stay valid until its work
+ * has run, and be ordered before it where another stream made it.  Strides count elements; the innermost
  * dimension is contiguous.  Arguments are checked before anything is launched; the text of a
  * failure is in mrf_last_error(NULL) of the calling thread.  Calls from several threads and on
  * several streams do not disturb one another as long as their outputs and workspaces are their
@@ -361,7 +362,8 @@ int mrf_launches_per_forward(const mrf_handle *h, int B, int T);
  * scale 0 and codes 0; a NaN makes its whole row's scales and codes NaN, an infinity its group's (the rest
  * of its row is 0).
  * out may be x, and residual_out may be residual (same pointer, stride and type); any other overlap is undefined.
- * Rows whose sum of squares passes the fp32 range are not supported (x beyond about 1e18).
+ * Rows whose sum of squares passes the fp32 range are not supported (x beyond about 1e18), nor an eps so small that
+ * rows below it in size but under about 1e-19 would count (their squares leave the range below).
  */
 typedef struct {
   const void *x;         /* dtype [rows, dim] */
@@ -449,12 +451,16 @@ mrf_status mrf_rope(const mrf_rope_args *a, void *stream);
  * device and held to the tensors' rows, so wrong ones give wrong rows but no access outside.
  *
  * F16 and BF16 with widths up to 128 run on the tensor cores when q, k, v and out are 16-byte
- * aligned with widths and strides that are multiples of 8 elements; anything else (F32, odd widths,
- * up to 256) runs on the CUDA cores.
+ * aligned with widths and strides that are multiples of 8 elements and above 0, with up to 128
+ * query heads a key head and with (q_rows + seqs) * kv_heads up to 33 million.  Anything else runs on the
+ * CUDA cores, 30 to 45 times slower in long prompts: F32, widths of 136 to 256, odd widths, heads off
+ * 16 bytes, and a key head that a stride of 0 repeats (pass it once: kv_heads is for that).
  *
  * workspace: device memory of at least the bytes mrf_attention_workspace gives for the same
  * arguments (which may be 0), 16-byte aligned, the call's own until the work has run.  max_k, an upper bound
- * of the sequences' key counts, decides only how the work is split, never the result's rows.
+ * of the sequences' key counts, decides only how the work is split, never the result's rows.  Long keys of few
+ * queries are split into ranges of a size that max_k gives, so the closer it is the better they fill the
+ * device: one token after 65536 keys takes 58 us with that bound, 76 with twice it and 250 with eight times.
  */
 typedef struct {
   const void *q, *k, *v;         /* dtype [q_rows, heads, width], [k_rows, kv_heads, width], [k_rows, kv_heads, v_width] */
